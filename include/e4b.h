@@ -477,6 +477,77 @@ E4B_API e4b_status e4b_moe_expert_forward_decode_noalloc(const uint16_t* x, int6
                                                          int renormalize, const e4b_expert_stack* w,
                                                          uint16_t* out, e4b_stream stream);
 
+/*
+ * The norms after and before a block (the expert layer above, or any other),
+ * fused with the block's gate, its residual scale and the residual sum.  The
+ * pages have no counterpart of this call; a decoder block is
+ *     x, n -> y = block(n) -> r, n' -> the next block
+ * and this call is the step between two blocks:
+ *     z = N(y; w_post)                          (z = y without w_post)
+ *     r = x + residual_scale * f(gate) * z      f(g) = g, or sigmoid(g)
+ *     n = N(r; w_next)                          (skipped without w_next)
+ *     N(v; w) = v / sqrt(mean(v^2) + eps) * (w + weight_offset)
+ * With y NULL it is the norm before the first block: n = N(x; w_next).
+ */
+typedef enum {
+  E4B_GATE_NONE = 0,    /* f = 1                                  */
+  E4B_GATE_CHANNEL = 1, /* gate [H]: a factor for each column     */
+  E4B_GATE_TOKEN = 2,   /* gate [M]: a factor for each row        */
+  E4B_GATE_FULL = 3     /* gate [M, H], contiguous                */
+} e4b_gate_kind;
+
+/* What the calls of one place in the model share. */
+typedef struct {
+  const void* w_post;    /* [H] of w_dtype, or NULL */
+  const void* w_next;    /* [H] of w_dtype, or NULL */
+  e4b_dtype w_dtype;
+  int32_t gate_sigmoid;  /* nonzero: f(g) = sigmoid(g) */
+  float eps;             /* > 0 */
+  float residual_scale;
+  float weight_offset;   /* 1 where weights are stored around zero */
+  int64_t H;             /* 1 .. 16384 */
+} e4b_block_norm;
+
+/*
+ * x, r [M, H] of x_dtype with leading dimensions ldx, ldr; y [M, H] of y_dtype
+ * (or NULL); n [M, H] of n_dtype; gate of gate_dtype in the shape of its kind.
+ * r is written exactly when y is given, n exactly when w_next is; types and
+ * leading dimensions of absent tensors are ignored.  Leading dimensions are in
+ * elements, >= H.  Rows of any width and alignment are taken; H and leading
+ * dimensions in multiples of 8 with 16-byte aligned bases are moved as vectors.
+ * r may be x and n may be y or x (same base, type and leading dimension).
+ * Sums and both norms are taken in fp32, n from the unrounded r; each output
+ * is rounded once.  M >= 0; no workspace; one launch.
+ */
+E4B_API e4b_status e4b_block_norm_forward(const void* x, e4b_dtype x_dtype, int64_t ldx, const void* y,
+                                          e4b_dtype y_dtype, int64_t ldy, const void* gate,
+                                          e4b_gate_kind gate_kind, e4b_dtype gate_dtype, int64_t M,
+                                          const e4b_block_norm* norm, void* r, int64_t ldr, void* n,
+                                          e4b_dtype n_dtype, int64_t ldn, e4b_stream stream);
+
+/*
+ * Gradients of sum(dr * r) + sum(dn * n) for the call above, from the r it
+ * wrote (with y NULL: from x, passed as r), y and gate:
+ *   dx      [M, H] of x_dtype    dy     [M, H] of y_dtype
+ *   dgate   E4B_GATE_CHANNEL: [H] fp32; TOKEN, FULL: gate's shape and type
+ *   dw_post, dw_next  [H] fp32
+ * dr [M, H] of x_dtype may be NULL (no gradient reaches r from elsewhere); dn
+ * [M, H] of n_dtype is given exactly when w_next is.  Any output may be NULL.
+ * dx may be dr and dy may be y (same base, type and leading dimension).
+ * Sums over rows are taken in a fixed order (deterministic).  M == 0 writes
+ * zeros to dw_post, dw_next and a channel gate's dgate.
+ * workspace  e4b_block_norm_backward_workspace_size() bytes; it needs no
+ *            initialisation and has no error word (no kernel here waits).
+ */
+E4B_API size_t e4b_block_norm_backward_workspace_size(int64_t M, const e4b_block_norm* norm);
+E4B_API e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn, e4b_dtype n_dtype,
+                                           int64_t lddn, const void* r, e4b_dtype x_dtype, int64_t ldr,
+                                           const void* y, e4b_dtype y_dtype, int64_t ldy, const void* gate,
+                                           e4b_gate_kind gate_kind, e4b_dtype gate_dtype, int64_t M,
+                                           const e4b_block_norm* norm, void* dx, int64_t lddx, void* dy,
+                                           int64_t lddy, void* dgate, float* dw_post, float* dw_next,
+                                           void* workspace, size_t workspace_bytes, e4b_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

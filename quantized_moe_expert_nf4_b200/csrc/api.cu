@@ -116,6 +116,10 @@ T* at(void* base, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(base) + off);
 }
 
+bool quant_type_ok(int q) { return q == E4B_QUANT_NF4 || q == E4B_QUANT_FP4; }
+
+}  // namespace
+
 e4b_status fail(e4b_status s, const std::string& msg) {
   g_error = msg;
   return s;
@@ -127,7 +131,6 @@ e4b_status cuda_fail(cudaError_t err, const char* where) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool quant_type_ok(int q) { return q == E4B_QUANT_NF4 || q == E4B_QUANT_FP4; }
 
 // Size, presence and alignment of a caller's workspace.
 e4b_status check_workspace(const char* what, size_t need, const void* workspace, size_t workspace_bytes) {
@@ -137,6 +140,8 @@ e4b_status check_workspace(const char* what, size_t need, const void* workspace,
     return fail(E4B_ERR_INVALID_ARGUMENT, std::string(what) + " workspace must be 16-byte aligned");
   return E4B_OK;
 }
+
+namespace {
 
 static_assert(kErrNone == E4B_KERNEL_ERR_NONE && kErrWaitFull == E4B_KERNEL_ERR_WAIT_FULL &&
                   kErrWaitEmpty == E4B_KERNEL_ERR_WAIT_EMPTY && kErrWaitDrain == E4B_KERNEL_ERR_WAIT_DRAIN &&

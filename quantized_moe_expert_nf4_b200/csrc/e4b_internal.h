@@ -35,6 +35,11 @@ void begin_call();  // resets the per-call launch counter
 // record the message (e4b_last_error) and return the status.
 e4b_status check_stack(const e4b_expert_stack* w, int k);  // stack pointers, shapes, alignment, LoRA rank, k
 e4b_status check_sm100();                                 // the current device is sm_100
+e4b_status fail(e4b_status s, const std::string& msg);    // records the message, returns the status
+e4b_status cuda_fail(cudaError_t err, const char* where);
+bool aligned16(const void* p);
+// Size, presence and alignment of a caller's workspace.
+e4b_status check_workspace(const char* what, size_t need, const void* workspace, size_t workspace_bytes);
 
 // The codebooks as the library holds them, indexed by e4b_quant_type: NF4
 // (QLoRA table, ascending) and FP4 (e2m1 / 6, in code order).

@@ -27,6 +27,7 @@ E4B_F32, E4B_BF16 = 0, 1
 E4B_EPI_NONE, E4B_EPI_SWIGLU = 0, 1
 E4B_PATH_AUTO, E4B_PATH_DECODE, E4B_PATH_GROUPED = 0, 1, 2
 E4B_QUANT_NF4, E4B_QUANT_FP4 = 0, 1
+E4B_GATE_NONE, E4B_GATE_CHANNEL, E4B_GATE_TOKEN, E4B_GATE_FULL = 0, 1, 2, 3
 # The E4B_VERSION this binding marshals for (e4b_expert_stack's layout among others).
 ABI_VERSION = 3
 
@@ -44,6 +45,7 @@ EXPORTED = (
     "e4b_moe_expert_forward_workspace_size", "e4b_moe_expert_forward",
     "e4b_moe_expert_forward_path", "e4b_moe_expert_forward_decode_noalloc",
     "e4b_moe_expert_backward_workspace_size", "e4b_moe_expert_backward",
+    "e4b_block_norm_forward", "e4b_block_norm_backward_workspace_size", "e4b_block_norm_backward",
 )
 
 
@@ -61,6 +63,14 @@ class ExpertStackC(ctypes.Structure):
         ("lora_r", ctypes.c_int), ("lora_alpha", ctypes.c_float),
         ("E", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64),
         ("quant_type", ctypes.c_int32),
+    ]
+
+
+class BlockNormC(ctypes.Structure):
+    _fields_ = [
+        ("w_post", ctypes.c_void_p), ("w_next", ctypes.c_void_p), ("w_dtype", ctypes.c_int),
+        ("gate_sigmoid", ctypes.c_int32), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+        ("weight_offset", ctypes.c_float), ("H", ctypes.c_int64),
     ]
 
 
@@ -149,6 +159,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.e4b_moe_expert_forward_path.restype = i32
     lib.e4b_moe_expert_forward_path.argtypes = [vp, i64, vp, i32, i32, ctypes.POINTER(ExpertStackC), vp, vp,
                                                 sz, i32, vp]
+    bn = ctypes.POINTER(BlockNormC)
+    lib.e4b_block_norm_forward.restype = i32
+    lib.e4b_block_norm_forward.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, i32, i64, bn, vp, i64, vp, i32, i64, vp]
+    lib.e4b_block_norm_backward_workspace_size.restype = sz
+    lib.e4b_block_norm_backward_workspace_size.argtypes = [i64, bn]
+    lib.e4b_block_norm_backward.restype = i32
+    lib.e4b_block_norm_backward.argtypes = [vp, i64, vp, i32, i64, vp, i32, i64, vp, i32, i64, vp, i32, i32, i64, bn, vp,
+                                            i64, vp, i64, vp, vp, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -512,6 +530,130 @@ def e4b_moe_expert_forward_decode_noalloc(x: torch.Tensor, router_logits: torch.
     _check(load_library().e4b_moe_expert_forward_decode_noalloc(
         x.data_ptr(), M, router_logits.data_ptr(), k, int(bool(renormalize)), ctypes.byref(stack.c),
         out.data_ptr(), _stream(stream)), "e4b_moe_expert_forward_decode_noalloc")
+
+
+_DTYPES = {torch.float32: E4B_F32, torch.bfloat16: E4B_BF16}
+
+
+def _launch(fn: str, device: torch.device, stream, *args) -> None:
+    """Calls `fn` on the tensors' device: on `stream`, or on that device's current stream."""
+    f = getattr(_lib or load_library(), fn)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(f(*args, _stream(stream)), fn)
+        return
+    status = f(*args, _stream(stream))
+    if status != E4B_OK:
+        _check(status, fn)
+
+
+def _rows(t: Optional[torch.Tensor], name: str, M: int, H: int, device: torch.device, dtype=None):
+    """(pointer, dtype code, leading dimension) of a tensor of rows; (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != H or (H > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{M}, {H}] with unit column stride")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    code = _DTYPES.get(t.dtype)
+    if code is None or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
+    # the stride of a single row says nothing
+    return t.data_ptr(), code, t.stride(0) if M > 1 else H
+
+
+class BlockNorm:
+    """What the calls of one place between two blocks share: the weights [H] of the norm after
+    the block and of the next block's norm (either may be None) and the constants."""
+
+    def __init__(self, H: int, w_post=None, w_next=None, eps: float = 1e-6, residual_scale: float = 1.0,
+                 weight_offset: float = 0.0, gate_sigmoid: bool = False):
+        weights = [w for w in (w_post, w_next) if w is not None]
+        for w, n in ((w_post, "w_post"), (w_next, "w_next")):
+            if w is None:
+                continue
+            _dev(w, n)
+            if tuple(w.shape) != (H,) or w.dtype not in _DTYPES or w.dtype != weights[0].dtype:
+                raise ValueError(f"{n} must be [H] in float32 or bfloat16, like the other weight")
+            if w.device != weights[0].device:
+                raise ValueError("w_post and w_next must be on one device")
+        self.tensors = (w_post, w_next)
+        self.device = weights[0].device if weights else None
+        self.H = int(H)
+        self.c = BlockNormC(_ptr(w_post), _ptr(w_next), _DTYPES[weights[0].dtype] if weights else E4B_F32,
+                            int(bool(gate_sigmoid)), float(eps), float(residual_scale), float(weight_offset), self.H)
+        self.ref = ctypes.byref(self.c)
+
+
+def _gate(gate: Optional[torch.Tensor], M: int, H: int, device: torch.device):
+    """(pointer, kind, dtype code) of a gate: [H] by channel, [M, 1] by token, [M, H] by element."""
+    if gate is None:
+        return None, E4B_GATE_NONE, 0
+    shape = tuple(gate.shape)
+    kind = {(H,): E4B_GATE_CHANNEL, (M, 1): E4B_GATE_TOKEN, (M, H): E4B_GATE_FULL}.get(shape)
+    if shape == (M, 1):
+        kind = E4B_GATE_TOKEN
+    if kind is None or not gate.is_contiguous() or gate.dtype not in _DTYPES:
+        raise ValueError("gate must be [H], [M, 1] or [M, H], contiguous, in float32 or bfloat16")
+    if gate.device != device:
+        raise ValueError(f"gate must be on {device}")
+    return gate.data_ptr(), kind, _DTYPES[gate.dtype]
+
+
+def _norm_device(t: torch.Tensor, norm: BlockNorm, name: str) -> torch.device:
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    if norm.device is not None and norm.device != t.device:
+        raise ValueError(f"{name} must be on the weights' device, {norm.device}")
+    return t.device
+
+
+def e4b_block_norm_forward(x: torch.Tensor, y: Optional[torch.Tensor], gate: Optional[torch.Tensor], norm: BlockNorm,
+                           r: Optional[torch.Tensor], n: Optional[torch.Tensor], stream=None) -> None:
+    """r = x + residual_scale * f(gate) * N(y; w_post) and n = N(r; w_next) (see include/e4b.h).  gate is
+    [H], [M, 1] or [M, H]; r is given exactly when y is, n exactly when the norm has w_next."""
+    dev = _norm_device(x, norm, "x")
+    M, H = x.shape[0], norm.H
+    xp, xd, ldx = _rows(x, "x", M, H, dev)
+    yp, yd, ldy = _rows(y, "y", M, H, dev)
+    gp, kind, gd = _gate(gate, M, H, dev)
+    rp, _, ldr = _rows(r, "r", M, H, dev, x.dtype)
+    np_, nd, ldn = _rows(n, "n", M, H, dev)
+    _launch("e4b_block_norm_forward", dev, stream, xp, xd, ldx, yp, yd, ldy, gp, kind, gd, M, norm.ref, rp, ldr, np_, nd,
+            ldn)
+
+
+def e4b_block_norm_backward_workspace_size(M: int, norm: BlockNorm) -> int:
+    return int(load_library().e4b_block_norm_backward_workspace_size(M, norm.ref))
+
+
+def e4b_block_norm_backward(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor], r: torch.Tensor,
+                            y: Optional[torch.Tensor], gate: Optional[torch.Tensor], norm: BlockNorm,
+                            dx: Optional[torch.Tensor], dy: Optional[torch.Tensor], dgate: Optional[torch.Tensor],
+                            dw_post: Optional[torch.Tensor], dw_next: Optional[torch.Tensor],
+                            workspace: Optional[torch.Tensor], stream=None) -> None:
+    """Gradients of sum(dr * r) + sum(dn * n) by x, y, gate and the weights (any output may be None)."""
+    dev = _norm_device(r, norm, "r")
+    M, H = r.shape[0], norm.H
+    rp, rd, ldr = _rows(r, "r", M, H, dev)
+    drp, _, lddr = _rows(dr, "dr", M, H, dev, r.dtype)
+    dnp, nd, lddn = _rows(dn, "dn", M, H, dev)
+    yp, yd, ldy = _rows(y, "y", M, H, dev)
+    gp, kind, gd = _gate(gate, M, H, dev)
+    dxp, _, lddx = _rows(dx, "dx", M, H, dev, r.dtype)
+    dyp, _, lddy = _rows(dy, "dy", M, H, dev, None if y is None else y.dtype)
+    for t, n in ((dw_post, "dw_post"), (dw_next, "dw_next")):
+        if t is not None:
+            _dev(t, n, torch.float32)
+            if t.numel() != H or t.device != dev:
+                raise ValueError(f"{n} must be [H] on {dev}")
+    if dgate is not None:
+        _dev(dgate, "dgate", torch.float32 if kind == E4B_GATE_CHANNEL else None if gate is None else gate.dtype)
+        if gate is None or dgate.shape != gate.shape or dgate.device != dev:
+            raise ValueError("dgate must have the gate's shape and device")
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("e4b_block_norm_backward", dev, stream, drp, lddr, dnp, nd, lddn, rp, rd, ldr, yp, yd, ldy, gp, kind, gd, M,
+            norm.ref, dxp, lddx, dyp, lddy, _ptr(dgate), _ptr(dw_post), _ptr(dw_next), _ptr(workspace), ws)
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:

@@ -1,0 +1,77 @@
+"""Refusals of the calls around the experts: checked on the host, before anything is launched (no GPU)."""
+import ctypes
+
+import pytest
+
+from quantized_moe_expert_nf4_b200 import e4b
+
+P = 1 << 20  # stands for a device pointer; never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+    if not os.path.exists(e4b.LIB_PATH):
+        from quantized_moe_expert_nf4_b200 import build
+        build.build()
+    return e4b.load_library()
+
+
+def _norm(**kw):
+    base = dict(w_post=P, w_next=P, w_dtype=1, gate_sigmoid=0, eps=1e-6, residual_scale=1.0, weight_offset=0.0, H=64)
+    return e4b.BlockNormC(*{**base, **kw}.values())
+
+
+def _norm_forward(lib, norm, x=P, xd=1, ldx=64, y=P, yd=1, ldy=64, gate=None, kind=0, gd=1, M=4, r=P, ldr=64, n=P, nd=1,
+                  ldn=64):
+    st = lib.e4b_block_norm_forward(x, xd, ldx, y, yd, ldy, gate, kind, gd, M, ctypes.byref(norm), r, ldr, n, nd, ldn, None)
+    return st, lib.e4b_last_error().decode()
+
+
+@pytest.mark.parametrize("norm,args,status,word", [
+    ({"H": 0}, {}, 2, "H must"), ({"H": 16385}, {}, 2, "H must"), ({"eps": 0.0}, {}, 1, "eps"),
+    ({"eps": float("nan")}, {}, 1, "eps"), ({"w_dtype": 2}, {}, 1, "w_dtype"), ({"w_post": P + 1}, {}, 1, "w_post"),
+    ({"w_dtype": 0, "w_next": P + 2}, {}, 1, "w_next"),
+    ({}, {"M": -1}, 1, "M must"), ({}, {"M": 1 << 31}, 1, "M must"), ({}, {"x": None}, 1, "null x"),
+    ({}, {"r": None}, 1, "r is written"), ({"w_post": None}, {"y": None}, 1, "r is written"),
+    ({}, {"n": None}, 1, "n is written"), ({"w_next": None}, {}, 1, "n is written"),
+    ({}, {"y": None, "r": None}, 1, "needs the block's output"),
+    ({"w_post": None, "w_next": None}, {"y": None, "r": None, "n": None}, 1, "nothing to compute"),
+    ({}, {"kind": 1}, 1, "gate and gate_kind"), ({}, {"gate": P}, 1, "gate and gate_kind"),
+    ({}, {"gate": P, "kind": 4}, 1, "unknown gate"), ({}, {"gate": P, "kind": 3, "gd": 5}, 1, "gate_dtype"),
+    ({}, {"gate": P + 1, "kind": 3}, 1, "gate"),
+    ({}, {"xd": 3}, 1, "x's type"), ({}, {"ldx": 63}, 1, "x's leading"), ({}, {"ldr": 10}, 1, "r's leading"),
+    ({}, {"y": P + 1}, 1, "y must be aligned"), ({}, {"xd": 0, "x": P + 2}, 1, "x must be aligned"),
+])
+def test_block_norm_forward(lib, norm, args, status, word):
+    st, msg = _norm_forward(lib, _norm(**norm), **args)
+    assert st == status and word in msg, msg
+
+
+def _norm_backward(lib, norm, dr=P, dn=P, r=P, y=P, gate=None, kind=0, M=4, dx=P, lddx=64, dy=P, dgate=None, dwp=P, dwn=P,
+                   ws=P, nbytes=1 << 30):
+    st = lib.e4b_block_norm_backward(dr, 64, dn, 1, 64, r, 1, 64, y, 1, 64, gate, kind, 1, M, ctypes.byref(norm), dx, lddx,
+                                     dy, 64, dgate, dwp, dwn, ws, nbytes, None)
+    return st, lib.e4b_last_error().decode()
+
+
+@pytest.mark.parametrize("norm,args,status,word", [
+    ({}, {"dn": None}, 1, "dn is read"), ({"w_next": None}, {}, 1, "dn is read"), ({}, {"r": None}, 1, "null r"),
+    ({"w_next": None}, {"dr": None, "dn": None, "dwn": None}, 1, "neither dr nor dn"),
+    ({"w_post": None}, {}, 1, "does not have"), ({}, {"dgate": P}, 1, "does not have"),
+    ({"w_post": None}, {"y": None, "dwp": None}, 1, "does not have"),
+    ({}, {"lddx": 8}, 1, "dx's leading"), ({}, {"dwp": P + 2}, 1, "dw_post"),
+    ({}, {"nbytes": 100}, 3, "workspace needs"), ({}, {"ws": None}, 3, "workspace needs"),
+    ({}, {"ws": P + 8}, 1, "workspace must be 16-byte aligned"),
+])
+def test_block_norm_backward(lib, norm, args, status, word):
+    st, msg = _norm_backward(lib, _norm(**norm), **args)
+    assert st == status and word in msg, msg
+
+
+def test_block_norm_workspace(lib):
+    size = lambda M, H: lib.e4b_block_norm_backward_workspace_size(M, ctypes.byref(_norm(H=H)))  # noqa: E731
+    assert size(0, 64) == 0 and size(4, 0) == 0 and size(4, 16385) == 0
+    assert size(1, 2048) == 3 * 2048 * 4                      # one row: one partial sum
+    assert size(1 << 30, 16384) <= 3 * 16384 * 4 * 148        # bounded by the grid, not by M
+    assert size(1 << 30, 8) <= 3 * 8 * 4 * 148 * 24
