@@ -90,8 +90,9 @@ typedef enum {
  */
 typedef enum {
   E4B_QUANT_NF4 = 0, /* the NF4 table of the QLoRA paper, ascending, entry 7 = 0 */
-  E4B_QUANT_FP4 = 1  /* e2m1 codes over 6: code c = (-1)^(c>>3) * m[c & 7] / 6 with
+  E4B_QUANT_FP4 = 1, /* e2m1 codes over 6: code c = (-1)^(c>>3) * m[c & 7] / 6 with
                         m = 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0 and 8 are zero) */
+  E4B_QUANT_INT4 = 3 /* e4b_gemv_4bit() only: code minus the group's zero point */
 } e4b_quant_type;
 
 /* Which implementation e4b_moe_expert_forward_path() runs. */
@@ -476,6 +477,42 @@ E4B_API e4b_status e4b_moe_expert_forward_decode_noalloc(const uint16_t* x, int6
                                                          const float* router_logits, int k,
                                                          int renormalize, const e4b_expert_stack* w,
                                                          uint16_t* out, e4b_stream stream);
+
+/*
+ * A dense 4-bit matrix with group scales: the projections and the shared
+ * expert of a model whose routed experts are the stacks above.
+ * Source: experts4bit-qlora 0.22.0, "Inference" (a fused 4-bit GEMV for single-token
+ * decode); Solutions -- one page per problem, the grouped-nf4-gemm row on
+ * gemv_int4_b32 (int4 in blocks of 32).
+ */
+typedef struct {
+  const uint8_t* packed;  /* [N, K/2]: byte j of a row holds elements 2j (high nibble) and 2j+1 */
+  const void* scales;     /* [N, K/group] of scale_dtype */
+  const uint8_t* zeros;   /* INT4: [N, K/group] zero points 0..15, or NULL for 8; else NULL */
+  e4b_dtype scale_dtype;
+  int32_t quant_type;     /* e4b_quant_type: value = codebook[code] * scale, or (code - zero) * scale */
+  int32_t group;          /* elements of a row that share a scale: 32, 64 or 128 */
+  int64_t N, K;
+} e4b_group_weight;
+
+/*
+ * Products of 1 to 16 tokens with such a matrix, in one launch:
+ *     y[m, n] = sum_k x[m, k] * W[n, k]
+ * E4B_EPI_NONE: out[m, n] = y[m, n]; E4B_EPI_SWIGLU: out[m, i] =
+ * SiLU(y[m, i]) * y[m, N/2 + i], i < N/2 (gate = first half of the rows).
+ * An NF4 or FP4 matrix with group 64 and fp32 scales is what
+ * e4b_quantize_stack() writes for one expert.
+ *
+ * x [M, ldx] bf16 (ldx >= K, ldx % 8 == 0); out [M, ldo] of out_dtype.
+ * Requires K a multiple of the group; any N >= 1, even with SwiGLU;
+ * 0 <= M <= 16 (longer inputs: e4b_grouped_4bit_gemm() with one group).
+ * fp32 accumulation; scales multiply group sums in fp32.  With bf16 output the
+ * NF4 and FP4 entries are rounded to bf16, as in the grouped GEMM; with fp32
+ * output they are exact to 2^-17.  Deterministic.  No workspace.
+ */
+E4B_API e4b_status e4b_gemv_4bit(const uint16_t* x, int64_t M, int64_t ldx, const e4b_group_weight* w,
+                                 e4b_epilogue epi, void* out, e4b_dtype out_dtype, int64_t ldo,
+                                 e4b_stream stream);
 
 /*
  * The norms after and before a block (the expert layer above, or any other),

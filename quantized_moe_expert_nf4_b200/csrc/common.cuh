@@ -54,6 +54,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + __expf(-z)); }
 
+// GELU in its tanh form: z/2 (1 + tanh(u)) = z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
+__device__ __forceinline__ float gelu_tanh_f32(float z) {
+  return z / (1.0f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+}
+
 template <typename T>
 __device__ __forceinline__ T clampv(T v, T lo, T hi) {
   return v < lo ? lo : (v > hi ? hi : v);

@@ -247,6 +247,28 @@ std::string decode_unsupported_reason(int64_t M, int64_t E, int k, int64_t H, in
 size_t decode_workspace_bytes(int64_t M, int64_t E, int k, int64_t H, int64_t I, int r);
 cudaError_t launch_decode_forward(const DecodeArgs& a, cudaStream_t stream);
 
+// ---- a few rows times a dense matrix -------------------------------------------
+enum { kGemvCodebook = 0, kGemvInt4 = 1, kGemvBf16 = 2 };       // weight formats
+enum { kGemvNone = 0, kGemvSilu = 1, kGemvGelu = 2 };           // epilogues; the last two gate: act(row i) * row N/2 + i
+struct GemvArgs {
+  const uint16_t* x;  // [M, ldx] bf16, 16-byte aligned rows
+  int64_t ldx;
+  int M;              // 1 .. 16
+  const void* w;      // [N, row_bytes]; row_bytes % 16 == 0
+  int64_t row_bytes;
+  int fmt, quant;     // quant: e4b_quant_type of a codebook
+  const void* scales; // [N, groups]
+  bool scale_f32;
+  const uint8_t* zeros;  // [N, groups] or null (8)
+  int group, groups;
+  int N, K;           // K % 8 == 0
+  int epi;
+  void* out;          // [M, ldo]
+  bool out_f32;
+  int64_t ldo;
+};
+cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream);
+
 // Device properties cached per device.
 struct DeviceInfo {
   int device;

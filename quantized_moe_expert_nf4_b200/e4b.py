@@ -26,7 +26,7 @@ STATUS_NAMES = {0: "E4B_OK", 1: "E4B_ERR_INVALID_ARGUMENT", 2: "E4B_ERR_UNSUPPOR
 E4B_F32, E4B_BF16 = 0, 1
 E4B_EPI_NONE, E4B_EPI_SWIGLU = 0, 1
 E4B_PATH_AUTO, E4B_PATH_DECODE, E4B_PATH_GROUPED = 0, 1, 2
-E4B_QUANT_NF4, E4B_QUANT_FP4 = 0, 1
+E4B_QUANT_NF4, E4B_QUANT_FP4, E4B_QUANT_INT4 = 0, 1, 3
 E4B_GATE_NONE, E4B_GATE_CHANNEL, E4B_GATE_TOKEN, E4B_GATE_FULL = 0, 1, 2, 3
 # The E4B_VERSION this binding marshals for (e4b_expert_stack's layout among others).
 ABI_VERSION = 3
@@ -45,6 +45,7 @@ EXPORTED = (
     "e4b_moe_expert_forward_workspace_size", "e4b_moe_expert_forward",
     "e4b_moe_expert_forward_path", "e4b_moe_expert_forward_decode_noalloc",
     "e4b_moe_expert_backward_workspace_size", "e4b_moe_expert_backward",
+    "e4b_gemv_4bit",
     "e4b_block_norm_forward", "e4b_block_norm_backward_workspace_size", "e4b_block_norm_backward",
 )
 
@@ -63,6 +64,14 @@ class ExpertStackC(ctypes.Structure):
         ("lora_r", ctypes.c_int), ("lora_alpha", ctypes.c_float),
         ("E", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64),
         ("quant_type", ctypes.c_int32),
+    ]
+
+
+class GroupWeightC(ctypes.Structure):
+    _fields_ = [
+        ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+        ("scale_dtype", ctypes.c_int), ("quant_type", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("N", ctypes.c_int64), ("K", ctypes.c_int64),
     ]
 
 
@@ -159,6 +168,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.e4b_moe_expert_forward_path.restype = i32
     lib.e4b_moe_expert_forward_path.argtypes = [vp, i64, vp, i32, i32, ctypes.POINTER(ExpertStackC), vp, vp,
                                                 sz, i32, vp]
+    lib.e4b_gemv_4bit.restype = i32
+    lib.e4b_gemv_4bit.argtypes = [vp, i64, i64, ctypes.POINTER(GroupWeightC), i32, vp, i32, i64, vp]
     bn = ctypes.POINTER(BlockNormC)
     lib.e4b_block_norm_forward.restype = i32
     lib.e4b_block_norm_forward.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, i32, i64, bn, vp, i64, vp, i32, i64, vp]
@@ -560,6 +571,41 @@ def _rows(t: Optional[torch.Tensor], name: str, M: int, H: int, device: torch.de
         raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
     # the stride of a single row says nothing
     return t.data_ptr(), code, t.stride(0) if M > 1 else H
+
+
+class GroupWeight:
+    """A dense 4-bit matrix [N, K] with a scale (and, for INT4, optionally a zero point) per group of a row."""
+
+    def __init__(self, packed: torch.Tensor, scales: torch.Tensor, N: int, K: int, group: int = 64,
+                 quant_type: int = E4B_QUANT_NF4, zeros: Optional[torch.Tensor] = None):
+        _dev(packed, "packed", torch.uint8)
+        _dev(scales, "scales")
+        if scales.dtype not in _DTYPES:
+            raise ValueError("scales must be float32 or bfloat16")
+        if group not in (32, 64, 128) or K % group:
+            raise ValueError("group must be 32, 64 or 128 and divide K")
+        if zeros is not None:
+            _dev(zeros, "zeros", torch.uint8)
+        if packed.numel() < N * K // 2 or scales.numel() < N * (K // group):
+            raise ValueError("packed or scales too small")
+        if zeros is not None and zeros.numel() < N * (K // group):
+            raise ValueError("zeros too small")
+        if any(t is not None and t.device != packed.device for t in (scales, zeros)):
+            raise ValueError("packed, scales and zeros must be on one device")
+        self.tensors = (packed, scales, zeros)
+        self.device, self.N, self.K = packed.device, int(N), int(K)
+        self.c = GroupWeightC(packed.data_ptr(), scales.data_ptr(), _ptr(zeros), _DTYPES[scales.dtype], int(quant_type),
+                              int(group), self.N, self.K)
+        self.ref = ctypes.byref(self.c)
+
+
+def e4b_gemv_4bit(x: torch.Tensor, weight: GroupWeight, out: torch.Tensor, epi: int = E4B_EPI_NONE, stream=None) -> None:
+    """out [M, N or N/2] = x [M, K] . W^T for 1 to 16 rows (see include/e4b.h)."""
+    dev = weight.device
+    M = x.shape[0]
+    xp, _, ldx = _rows(x, "x", M, weight.K, dev, torch.bfloat16)
+    op, od, ldo = _rows(out, "out", M, weight.N // 2 if epi == E4B_EPI_SWIGLU else weight.N, dev)
+    _launch("e4b_gemv_4bit", dev, stream, xp, M, ldx, weight.ref, epi, op, od, ldo)
 
 
 class BlockNorm:

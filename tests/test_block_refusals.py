@@ -75,3 +75,31 @@ def test_block_norm_workspace(lib):
     assert size(1, 2048) == 3 * 2048 * 4                      # one row: one partial sum
     assert size(1 << 30, 16384) <= 3 * 16384 * 4 * 148        # bounded by the grid, not by M
     assert size(1 << 30, 8) <= 3 * 8 * 4 * 148 * 24
+
+
+def _gemv(lib, weight=None, x=P, M=2, ldx=128, epi=0, out=P, od=1, ldo=64):
+    base = dict(packed=P, scales=P, zeros=None, scale_dtype=0, quant_type=0, group=64, N=64, K=128)
+    w = e4b.GroupWeightC(*{**base, **(weight or {})}.values())
+    st = lib.e4b_gemv_4bit(x, M, ldx, ctypes.byref(w), epi, out, od, ldo, None)
+    return st, lib.e4b_last_error().decode()
+
+
+@pytest.mark.parametrize("weight,args,status,word", [
+    ({"quant_type": 2}, {}, 1, "quant_type"), ({"quant_type": 4}, {}, 1, "quant_type"), ({"group": 16}, {}, 2, "group must"),
+    ({"group": 96}, {}, 2, "group must"), ({"K": 96}, {}, 2, "K must"), ({"K": 0}, {}, 2, "K must"), ({"N": 0}, {}, 2, "N must"),
+    ({"N": 1 << 30}, {}, 2, "N must"), ({"K": 1 << 30}, {}, 2, "K must"),
+    ({"scale_dtype": 2}, {}, 1, "scale_dtype"), ({"zeros": P}, {}, 1, "zero points"), ({"packed": None}, {}, 1, "null packed"),
+    ({"scales": P + 4}, {}, 1, "16-byte"), ({"quant_type": 3, "zeros": P + 1}, {}, 1, "16-byte"),
+    ({}, {"epi": 2}, 1, "epilogue"), ({"N": 63}, {"epi": 1}, 1, "even"), ({}, {"od": 4}, 1, "out_dtype"),
+    ({}, {"M": 17}, 2, "M must"), ({}, {"M": -1}, 2, "M must"), ({}, {"x": None}, 1, "null x"), ({}, {"out": None}, 1, "null x"),
+    ({}, {"ldx": 120}, 1, "ldx"), ({}, {"ldx": 132}, 1, "ldx"), ({}, {"ldo": 63}, 1, "ldo"), ({}, {"ldo": 31, "epi": 1}, 1, "ldo"),
+    ({}, {"x": P + 2}, 1, "16-byte"), ({}, {"out": P + 8}, 1, "16-byte"),
+])
+def test_gemv(lib, weight, args, status, word):
+    st, msg = _gemv(lib, weight, **args)
+    assert st == status and word in msg, msg
+
+
+def test_other_calls_take_no_int4(lib):
+    st = lib.e4b_grouped_4bit_gemm(P, 4, 64, None, P, 1, 4, P, P, 3, 64, 64, None, None, 0, 0.0, 0, P, 1, P, 1 << 20, None)
+    assert st == 1 and b"quant_type" in lib.e4b_last_error()
