@@ -585,6 +585,52 @@ E4B_API e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const v
                                            int64_t lddy, void* dgate, float* dw_post, float* dw_next,
                                            void* workspace, size_t workspace_bytes, e4b_stream stream);
 
+/*
+ * A dense gated feed-forward block in bf16: the shared expert, or the layers
+ * without experts, of a model that trains around frozen 4-bit experts.
+ * Source: experts4bit-qlora 0.22.0, "Scope" (the SwiGLU expert MLP), for a
+ * single dense expert whose weights are trained.
+ *     pre = x . gate_up^T,  h = act(pre[:, :I]) * pre[:, I:],  out = h . down^T
+ */
+typedef enum {
+  E4B_ACT_SILU = 0,     /* z * sigmoid(z) */
+  E4B_ACT_GELU_TANH = 1 /* z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+} e4b_activation;
+
+typedef struct {
+  const uint16_t* gate_up; /* [2I, H] bf16: gate rows, then up rows */
+  const uint16_t* down;    /* [H, I] bf16 */
+  int64_t H, I;            /* multiples of 8 */
+  int32_t act;             /* e4b_activation */
+} e4b_gated_ffn;
+
+/*
+ * x [M, ldx] bf16 (ldx >= H, ldx % 8 == 0), out [M, H] bf16.  pre [M, 2I]
+ * bf16, or NULL: the pre-activations, which the backward needs.  Any M >= 0.
+ * fp32 accumulation; h (and pre) are rounded to bf16 once.  Two launches.
+ * workspace  e4b_gated_ffn_forward_workspace_size() bytes, error word first.
+ */
+E4B_API size_t e4b_gated_ffn_forward_workspace_size(int64_t M, const e4b_gated_ffn* w);
+E4B_API e4b_status e4b_gated_ffn_forward(const uint16_t* x, int64_t M, int64_t ldx, const e4b_gated_ffn* w,
+                                         uint16_t* out, uint16_t* pre, void* workspace, size_t workspace_bytes,
+                                         e4b_stream stream);
+
+/*
+ * Gradients of sum(dout * out), dout [M, H] bf16, from the x and pre of the
+ * forward:  dx [M, H], dgate_up [2I, H], ddown [H, I], all bf16; any of the
+ * three may be NULL and is then not computed.  h is computed again from pre.
+ * All sums are fp32 in a fixed order (deterministic); h and the gradients by
+ * the pre-activations are rounded to bf16 between the products, so a wider
+ * type of the results would hold no more.  M == 0 writes zeros to the
+ * weights' gradients.  Up to four launches.
+ * workspace  e4b_gated_ffn_backward_workspace_size() bytes, error word first.
+ */
+E4B_API size_t e4b_gated_ffn_backward_workspace_size(int64_t M, const e4b_gated_ffn* w);
+E4B_API e4b_status e4b_gated_ffn_backward(const uint16_t* x, int64_t M, int64_t ldx, const e4b_gated_ffn* w,
+                                          const uint16_t* pre, const uint16_t* dout, uint16_t* dx,
+                                          uint16_t* dgate_up, uint16_t* ddown, void* workspace,
+                                          size_t workspace_bytes, e4b_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,7 @@ E4B_F32, E4B_BF16 = 0, 1
 E4B_EPI_NONE, E4B_EPI_SWIGLU = 0, 1
 E4B_PATH_AUTO, E4B_PATH_DECODE, E4B_PATH_GROUPED = 0, 1, 2
 E4B_QUANT_NF4, E4B_QUANT_FP4, E4B_QUANT_INT4 = 0, 1, 3
+E4B_ACT_SILU, E4B_ACT_GELU_TANH = 0, 1
 E4B_GATE_NONE, E4B_GATE_CHANNEL, E4B_GATE_TOKEN, E4B_GATE_FULL = 0, 1, 2, 3
 # The E4B_VERSION this binding marshals for (e4b_expert_stack's layout among others).
 ABI_VERSION = 3
@@ -47,6 +48,8 @@ EXPORTED = (
     "e4b_moe_expert_backward_workspace_size", "e4b_moe_expert_backward",
     "e4b_gemv_4bit",
     "e4b_block_norm_forward", "e4b_block_norm_backward_workspace_size", "e4b_block_norm_backward",
+    "e4b_gated_ffn_forward_workspace_size", "e4b_gated_ffn_forward",
+    "e4b_gated_ffn_backward_workspace_size", "e4b_gated_ffn_backward",
 )
 
 
@@ -80,6 +83,13 @@ class BlockNormC(ctypes.Structure):
         ("w_post", ctypes.c_void_p), ("w_next", ctypes.c_void_p), ("w_dtype", ctypes.c_int),
         ("gate_sigmoid", ctypes.c_int32), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
         ("weight_offset", ctypes.c_float), ("H", ctypes.c_int64),
+    ]
+
+
+class GatedFFNC(ctypes.Structure):
+    _fields_ = [
+        ("gate_up", ctypes.c_void_p), ("down", ctypes.c_void_p), ("H", ctypes.c_int64), ("I", ctypes.c_int64),
+        ("act", ctypes.c_int32),
     ]
 
 
@@ -178,6 +188,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.e4b_block_norm_backward.restype = i32
     lib.e4b_block_norm_backward.argtypes = [vp, i64, vp, i32, i64, vp, i32, i64, vp, i32, i64, vp, i32, i32, i64, bn, vp,
                                             i64, vp, i64, vp, vp, vp, vp, sz, vp]
+    ff = ctypes.POINTER(GatedFFNC)
+    lib.e4b_gated_ffn_forward_workspace_size.restype = sz
+    lib.e4b_gated_ffn_forward_workspace_size.argtypes = [i64, ff]
+    lib.e4b_gated_ffn_forward.restype = i32
+    lib.e4b_gated_ffn_forward.argtypes = [vp, i64, i64, ff, vp, vp, vp, sz, vp]
+    lib.e4b_gated_ffn_backward_workspace_size.restype = sz
+    lib.e4b_gated_ffn_backward_workspace_size.argtypes = [i64, ff]
+    lib.e4b_gated_ffn_backward.restype = i32
+    lib.e4b_gated_ffn_backward.argtypes = [vp, i64, i64, ff, vp, vp, vp, vp, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -573,6 +592,15 @@ def _rows(t: Optional[torch.Tensor], name: str, M: int, H: int, device: torch.de
     return t.data_ptr(), code, t.stride(0) if M > 1 else H
 
 
+def _workspace_arg(workspace: Optional[torch.Tensor], device: torch.device):
+    """(pointer, bytes) of a workspace."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 class GroupWeight:
     """A dense 4-bit matrix [N, K] with a scale (and, for INT4, optionally a zero point) per group of a row."""
 
@@ -697,9 +725,66 @@ def e4b_block_norm_backward(dr: Optional[torch.Tensor], dn: Optional[torch.Tenso
         _dev(dgate, "dgate", torch.float32 if kind == E4B_GATE_CHANNEL else None if gate is None else gate.dtype)
         if gate is None or dgate.shape != gate.shape or dgate.device != dev:
             raise ValueError("dgate must have the gate's shape and device")
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wp, ws = _workspace_arg(workspace, dev)
     _launch("e4b_block_norm_backward", dev, stream, drp, lddr, dnp, nd, lddn, rp, rd, ldr, yp, yd, ldy, gp, kind, gd, M,
-            norm.ref, dxp, lddx, dyp, lddy, _ptr(dgate), _ptr(dw_post), _ptr(dw_next), _ptr(workspace), ws)
+            norm.ref, dxp, lddx, dyp, lddy, _ptr(dgate), _ptr(dw_post), _ptr(dw_next), wp, ws)
+
+
+class GatedFFN:
+    """Weights of a dense gated feed-forward block: gate_up [2I, H] and down [H, I] in bf16."""
+
+    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, act: int = E4B_ACT_SILU):
+        _dev(gate_up, "gate_up", torch.bfloat16)
+        _dev(down, "down", torch.bfloat16)
+        if gate_up.dim() != 2 or down.dim() != 2 or tuple(gate_up.shape) != (2 * down.shape[1], down.shape[0]):
+            raise ValueError("gate_up must be [2I, H] and down [H, I]")
+        if gate_up.device != down.device:
+            raise ValueError("gate_up and down must be on one device")
+        self.tensors = (gate_up, down)
+        self.device, self.H, self.I = down.device, down.shape[0], down.shape[1]
+        self.c = GatedFFNC(gate_up.data_ptr(), down.data_ptr(), self.H, self.I, int(act))
+        self.ref = ctypes.byref(self.c)
+
+
+def _plain(t: Optional[torch.Tensor], name: str, shape, dtype, device: torch.device) -> Optional[int]:
+    """Pointer of a contiguous tensor of this shape, type and device; None for None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def e4b_gated_ffn_forward_workspace_size(M: int, ffn: GatedFFN) -> int:
+    return int(load_library().e4b_gated_ffn_forward_workspace_size(M, ffn.ref))
+
+
+def e4b_gated_ffn_forward(x: torch.Tensor, ffn: GatedFFN, out: torch.Tensor, pre: Optional[torch.Tensor],
+                          workspace: Optional[torch.Tensor], stream=None) -> None:
+    """out = (act(g) * u) . down^T with [g | u] = x . gate_up^T; pre [M, 2I], if given, takes [g | u]."""
+    dev, M = ffn.device, x.shape[0]
+    xp, _, ldx = _rows(x, "x", M, ffn.H, dev, torch.bfloat16)
+    op = _plain(out, "out", (M, ffn.H), torch.bfloat16, dev)
+    pp = _plain(pre, "pre", (M, 2 * ffn.I), torch.bfloat16, dev)
+    wp, ws = _workspace_arg(workspace, dev)
+    _launch("e4b_gated_ffn_forward", dev, stream, xp, M, ldx, ffn.ref, op, pp, wp, ws)
+
+
+def e4b_gated_ffn_backward_workspace_size(M: int, ffn: GatedFFN) -> int:
+    return int(load_library().e4b_gated_ffn_backward_workspace_size(M, ffn.ref))
+
+
+def e4b_gated_ffn_backward(x: torch.Tensor, ffn: GatedFFN, pre: torch.Tensor, dout: torch.Tensor,
+                           dx: Optional[torch.Tensor], dgate_up: Optional[torch.Tensor], ddown: Optional[torch.Tensor],
+                           workspace: Optional[torch.Tensor], stream=None) -> None:
+    """Gradients of sum(dout * out) by x and the weights, in bf16 (any of them may be None)."""
+    dev, M, H, I = ffn.device, x.shape[0], ffn.H, ffn.I
+    xp, _, ldx = _rows(x, "x", M, H, dev, torch.bfloat16)
+    bf = torch.bfloat16
+    wp, ws = _workspace_arg(workspace, dev)
+    _launch("e4b_gated_ffn_backward", dev, stream, xp, M, ldx, ffn.ref, _plain(pre, "pre", (M, 2 * I), bf, dev),
+            _plain(dout, "dout", (M, H), bf, dev), _plain(dx, "dx", (M, H), bf, dev),
+            _plain(dgate_up, "dgate_up", (2 * I, H), bf, dev), _plain(ddown, "ddown", (H, I), bf, dev), wp, ws)
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:

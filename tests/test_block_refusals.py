@@ -103,3 +103,43 @@ def test_gemv(lib, weight, args, status, word):
 def test_other_calls_take_no_int4(lib):
     st = lib.e4b_grouped_4bit_gemm(P, 4, 64, None, P, 1, 4, P, P, 3, 64, 64, None, None, 0, 0.0, 0, P, 1, P, 1 << 20, None)
     assert st == 1 and b"quant_type" in lib.e4b_last_error()
+
+
+def _ffn(**kw):
+    base = dict(gate_up=P, down=P, H=64, I=64, act=0)
+    return e4b.GatedFFNC(*{**base, **kw}.values())
+
+
+@pytest.mark.parametrize("ffn,args,status,word", [
+    ({"H": 0}, {}, 2, "H and I"), ({"H": 60}, {}, 2, "H and I"), ({"I": 4}, {}, 2, "H and I"), ({"I": 1 << 21}, {}, 2, "H and I"),
+    ({"act": 2}, {}, 1, "activation"), ({"gate_up": None}, {}, 1, "null gate_up"), ({"down": P + 2}, {}, 1, "16-byte"),
+    ({}, {"M": -1}, 2, "M must"), ({}, {"M": (1 << 24) + 1}, 2, "M must"), ({}, {"ldx": 56}, 1, "ldx"), ({}, {"ldx": 68}, 1, "ldx"),
+    ({}, {"x": None}, 1, "null x"), ({}, {"x": P + 8}, 1, "x must"), ({}, {"out": None}, 1, "null out"),
+    ({}, {"pre": P + 8}, 1, "out and pre"), ({}, {"nbytes": 256 + 4 * 64 * 2 - 1}, 3, "workspace needs"),
+    ({}, {"ws": None}, 3, "workspace needs"), ({}, {"ws": P + 4}, 1, "workspace must be"),
+])
+def test_gated_ffn_forward(lib, ffn, args, status, word):
+    a = dict(x=P, M=4, ldx=64, out=P, pre=None, ws=P, nbytes=1 << 20)
+    a.update(args)
+    st = lib.e4b_gated_ffn_forward(a["x"], a["M"], a["ldx"], ctypes.byref(_ffn(**ffn)), a["out"], a["pre"], a["ws"],
+                                   a["nbytes"], None)
+    assert st == status and word in lib.e4b_last_error().decode()
+
+
+@pytest.mark.parametrize("args,status,word", [
+    ({"pre": None}, 1, "null pre"), ({"dout": None}, 1, "null pre or dout"), ({"dx": P + 2}, 1, "gradients must"),
+    ({"dgu": P + 8}, 1, "gradients must"), ({"nbytes": 256 + 3 * 512 - 1}, 3, "workspace needs"), ({"x": None}, 1, "null x"),
+])
+def test_gated_ffn_backward(lib, args, status, word):
+    a = dict(x=P, pre=P, dout=P, dx=P, dgu=P, dd=P, nbytes=1 << 20)
+    a.update(args)
+    st = lib.e4b_gated_ffn_backward(a["x"], 4, 64, ctypes.byref(_ffn()), a["pre"], a["dout"], a["dx"], a["dgu"], a["dd"], P,
+                                    a["nbytes"], None)
+    assert st == status and word in lib.e4b_last_error().decode()
+
+
+def test_gated_ffn_workspaces(lib):
+    f = _ffn(H=2048, I=1000)
+    assert lib.e4b_gated_ffn_forward_workspace_size(0, ctypes.byref(f)) == 0
+    assert lib.e4b_gated_ffn_forward_workspace_size(3, ctypes.byref(f)) == 256 + (3 * 1000 * 2 + 255) // 256 * 256
+    assert lib.e4b_gated_ffn_backward_workspace_size(3, ctypes.byref(f)) >= 256 + 3 * 3 * 1000 * 2
