@@ -38,8 +38,6 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;
-constexpr int kStages = 4;               // 2 KB pieces in flight per warp
-constexpr uint32_t kPiece = 16 * 128;    // 16 rows x 128 bytes
 
 enum Fmt { kFmtCodebook = 0, kFmtInt4 = 1, kFmtBf16 = 2 };
 
@@ -48,7 +46,7 @@ struct Params {
   int chunks;     // ceil(row bytes / 128)
   int kw;         // warps that share a row tile
   int split;      // CTAs of a cluster that share a row tile
-  int tiles;      // CTA tiles of 16 * (8 / kw) rows
+  int tiles;      // CTA tiles of 16 RT * (8 / kw) rows
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -59,6 +57,14 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t v[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -72,38 +78,18 @@ __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32
 // rows give eight places for one unit, and two adjacent rows' four units do not meet.
 __device__ __forceinline__ uint32_t swz(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
 
-// Codebook bytes: word j / 4 byte j % 4 of lo / hi = low / high byte of bf16(entry j).
-struct Book {
-  uint32_t lo[4], hi[4];
-};
-
-// The entries' bf16 values (residual false), or bf16 of what that rounding left.
-__device__ __forceinline__ Book make_book(int quant, bool residual) {
-  Book t{};
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    float v = codebook_entry(quant, j);
-    if (residual) v -= bf16_bits_to_float(float_to_bf16_bits(v));
-    const uint32_t b = float_to_bf16_bits(v);
-    t.lo[j >> 2] |= (b & 0xffu) << (8 * (j & 3));
-    t.hi[j >> 2] |= (b >> 8) << (8 * (j & 3));
-  }
-  return t;
-}
-
-// Eight codes (byte i: element 2i in the high nibble) -> four bf16 pairs in
-// element order.  A byte permute looks up entries 0-7 or 8-15 of four codes at
-// once; `pick` keeps, per code, the half that its top bit names.
-__device__ __forceinline__ void decode_book(uint32_t w, const Book& t, uint32_t v[4]) {
-  const uint32_t s = w & 0x77777777u, pick = ((w >> 1) & 0x44444444u) | 0x32103210u;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t sh = s >> (16 * h), ph = pick >> (16 * h);
-    const uint32_t lo = __byte_perm(__byte_perm(t.lo[0], t.lo[1], sh), __byte_perm(t.lo[2], t.lo[3], sh), ph);
-    const uint32_t hi = __byte_perm(__byte_perm(t.hi[0], t.hi[1], sh), __byte_perm(t.hi[2], t.hi[3], sh), ph);
-    v[2 * h] = __byte_perm(lo, hi, 0x4051u);
-    v[2 * h + 1] = __byte_perm(lo, hi, 0x6273u);
-  }
+// Eight codebook codes (byte i: element 2i in the high nibble) -> four bf16 pairs in
+// element order, one table lookup per byte.  The table holds each byte's pair once
+// per lane (entry b of lane l at byte 128 b + 4 l), so lookups never share a
+// bank; `lane_table` is the table's shared address + 4 l, its low 15 bits 4 l.
+// Two integer instructions and one shared load per pair measured 2x faster in
+// the mainloop than byte permutes over the codebook in registers (21 integer
+// instructions per word, on a pipe of half the issue rate).
+__device__ __forceinline__ void decode_table(uint32_t w, uint32_t lane_table, uint32_t v[4]) {
+  v[0] = lds32(((w << 7) & 0x7f80u) + lane_table);
+  v[1] = lds32(((w >> 1) & 0x7f80u) + lane_table);
+  v[2] = lds32(((w >> 9) & 0x7f80u) + lane_table);
+  v[3] = lds32(((w >> 17) & 0x7f80u) + lane_table);
 }
 
 // Eight int4 codes -> bf16 pairs of elements (1, 5), (0, 4), (3, 7), (2, 6), each
@@ -117,217 +103,279 @@ __device__ __forceinline__ void decode_int4(uint32_t w, uint32_t zz, uint32_t v[
   }
 }
 
-template <int FMT>
-struct Traits {
+// FMT: weight format; GB: blocks of 32 k in a group; NT: sets of 8 tokens; RT: row
+// tiles of 16 per warp; TWO: codebook entries as two bf16 values.
+template <int FMT, int GB, int NT, int RT, bool TWO>
+struct Cfg {
   static constexpr int kBlocks = FMT == kFmtBf16 ? 2 : 8;   // blocks of 32 k in a chunk
   static constexpr int kChunkK = kBlocks * 32;
+  static constexpr int kGroups = FMT == kFmtBf16 ? 1 : kBlocks / GB;  // groups in a chunk
+  static constexpr uint32_t kPiece = RT * 16 * 128;
+  // Pieces in flight per warp: 64 KB per CTA, less beside two tables.
+  static constexpr int kStages = TWO ? 2 : 4 / RT;
+  static constexpr uint32_t kTable = FMT == kFmtCodebook ? 256 * 128 : 0;
+  static constexpr uint32_t kTables = kTable * (TWO ? 2 : 1);
+  static constexpr uint32_t kSmem = kTables + kWarps * kStages * kPiece;
 };
 
-// FMT: weight format; GB: blocks of 32 k in a group; NT: sets of 8 tokens;
-// TWO: codebook entries as two bf16 values.
-template <int FMT, int GB, int NT, bool TWO>
-__global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(Params p) {
-  using Tr = Traits<FMT>;
-  constexpr int NB = Tr::kBlocks;
+template <int FMT, int GB, int NT, int RT, bool TWO>
+__global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<FMT, GB, NT, RT, TWO>;
+  constexpr int NB = C::kBlocks, NG = C::kGroups, KS = C::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ float red[2][kWarps][NT][4][32];
+  __shared__ float red[2][kWarps][RT][NT][4][32];
   const GemvArgs& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int kw = p.kw, wk = warp % kw, wr = warp / kw;  // this warp's share of K, its row tile of the CTA's
+  const int kw = p.kw, wk = warp % kw, wr = warp / kw;  // this warp's share of K, its row tiles of the CTA's
   const int rank = p.split > 1 ? static_cast<int>(blockIdx.x % p.split) : 0;
   const int cta = p.split > 1 ? static_cast<int>(blockIdx.x / p.split) : static_cast<int>(blockIdx.x);
   const int ctas = static_cast<int>(gridDim.x) / p.split;
   const int first = rank * kw + wk, stride = kw * p.split;  // chunks first, first + stride, ...
   const bool glu = a.epi != kGemvNone;
   const int half = a.N / 2;
-  const int rows_out = glu ? 8 : 16;         // output columns of a warp's row tile
+  const int rows_out = glu ? 8 : 16;         // output columns of a row tile of 16 weight rows
   const int nout = glu ? half : a.N;
-  const int tile_out = rows_out * (kWarps / kw);
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * kStages * kPiece;
-  const unsigned char* ring_p = smem + warp * kStages * kPiece;
+  const int warp_out = rows_out * RT, tile_out = warp_out * (kWarps / kw);
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const uint32_t ring = base + C::kTables + warp * KS * C::kPiece;
 
-  // Weight row of MMA row r (0..15) of this warp's part of a tile: rows 8..15 are
-  // the up rows of a gated product.  Rows past the end read row 0, and are not written.
-  auto weight_row = [&](int tile, int r, bool* in) -> int64_t {
-    const int o = tile * tile_out + wr * rows_out + (glu ? (r & 7) : r);
-    *in = o < nout;
-    if (!*in) return 0;
-    return glu && r >= 8 ? half + o : o;
+  // Row tile j of a tile: MMA rows 0..15 are weight rows o .. o + 15, or the gate
+  // rows o .. o + 7 and the up rows half + o .. half + o + 7 of a gated product.
+  // Rows past the end read zeros, and are not written.
+
+  // This warp's pieces, in order: every chunk of its share, tile after tile.
+  // Lane l copies the 16-byte unit l % 8 of rows l / 8 + 4 i.
+  int put_tile = cta, put_chunk = first, put_stage = 0, put_o = 0;
+  const unsigned char* put_p = nullptr;
+  const int64_t rb4 = a.row_bytes * 4, rb_up = static_cast<int64_t>(half) * a.row_bytes;
+  const uint32_t put_dst = (lane >> 3) * 128;
+  auto put_rows = [&]() {
+    put_o = put_tile * tile_out + wr * warp_out + (lane >> 3);
+    put_p = static_cast<const unsigned char*>(a.w) + put_o * a.row_bytes + (lane & 7) * 16;
   };
-
-  // The pieces of this warp, in order: every chunk of its share, tile after tile.
-  int put_tile = cta, put_chunk = first;
-  int put_stage = 0;
   auto put = [&]() {
     if (put_tile < p.tiles && first < p.chunks) {
+      const int64_t off = static_cast<int64_t>(put_chunk) * 128;
+      const bool in_k = off + (lane & 7) * 16 < a.row_bytes;
+      const uint32_t dst = ring + put_stage * C::kPiece + put_dst;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 4 + (lane >> 3), u = lane & 7;
-        bool in;
-        const int64_t row = weight_row(put_tile, r, &in);
-        const int64_t off = static_cast<int64_t>(put_chunk) * 128 + u * 16;
-        in = in && off < a.row_bytes;
-        cp_async16(ring + put_stage * kPiece + r * 128 + ((u ^ swz(r)) << 4),
-                   static_cast<const unsigned char*>(a.w) + (in ? row * a.row_bytes + off : 0), in);
+      for (int i = 0; i < 4 * RT; ++i) {
+        // r: row within its row tile, less lane / 8
+        const int r = (i & 3) * 4, steps = glu ? (i >> 2) * 2 + (i & 1) : i;  // of 4 rows
+        const bool in = in_k && put_o + steps * 4 < nout;
+        const unsigned char* src = put_p + off + steps * rb4 + (glu && (i & 2) ? rb_up : 0);
+        cp_async16(dst + i * 512 + (((lane & 7) ^ swz(r + (lane >> 3))) << 4), in ? src : a.w, in);
       }
       put_chunk += stride;
       if (put_chunk >= p.chunks) {
         put_chunk = first;
         put_tile += ctas;
+        put_rows();
       }
     }
     cp_async_commit();
-    put_stage = put_stage + 1 == kStages ? 0 : put_stage + 1;
+    put_stage = put_stage + 1 == KS ? 0 : put_stage + 1;
   };
+  put_rows();
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) put();
+  for (int s = 0; s < KS - 1; ++s) put();
 
-  Book book{}, rest{};
-  if constexpr (FMT == kFmtCodebook) {
-    book = make_book(a.quant, false);
-    if constexpr (TWO) rest = make_book(a.quant, true);
-  }
+  // Scales (and zero points) of a chunk's NG groups, rows g and g + 8: lane t of the
+  // row's four keeps SPL of them and hands them over by shuffles, so that a
+  // chunk's can be loaded while the one before it is multiplied.
+  constexpr int SPL = NG > 4 ? NG / 4 : 1;
+  float ns[RT][2][SPL];
+  uint32_t nz[RT][2][SPL];
+  int64_t s_row[RT][2];
+  auto scale_rows = [&](int tile) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int o = tile * tile_out + wr * warp_out + j * rows_out + g + (glu ? 0 : 8 * h);
+        s_row[j][h] = o < nout ? static_cast<int64_t>(glu && h ? half + o : o) * a.groups : 0;
+      }
+  };
+  auto load_scales = [&](int chunk) {
+    if constexpr (FMT != kFmtBf16) {
+#pragma unroll
+      for (int i = 0; i < SPL; ++i) {
+        const int grp = chunk * NG + (t % (NG / SPL)) * SPL + i;
+        const bool in = grp < a.groups;  // zero past K
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t at = s_row[j][h] + (in ? grp : 0);
+            const float v = a.scale_f32 ? static_cast<const float*>(a.scales)[at]
+                                        : bf16_bits_to_float(static_cast<const uint16_t*>(a.scales)[at]);
+            ns[j][h][i] = in ? v : 0.0f;
+            if constexpr (FMT == kFmtInt4) nz[j][h][i] = a.zeros ? a.zeros[at] & 15u : 8u;
+          }
+      }
+    }
+  };
+  scale_rows(cta < p.tiles ? cta : 0);
+  load_scales(first);
+
   uint32_t x[NT][NB][4];
   int x_chunk = -1;
-  int stage = 0, buf = 0;
-  for (int tile = cta; tile < p.tiles; tile += ctas, buf ^= 1) {
-    float acc[NT][4] = {};
-    bool in0, in1;
-    const int64_t row0 = weight_row(tile, g, &in0), row1 = weight_row(tile, g + 8, &in1);
-    for (int chunk = first; chunk < p.chunks; chunk += stride) {
-      if (chunk != x_chunk) {
-        x_chunk = chunk;
+  const uint16_t* x_lane = a.x + g * a.ldx + t * 8;
+  auto load_x = [&](int chunk) {
+    x_chunk = chunk;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const int k = chunk * Tr::kChunkK + b * 32 + t * 8;
-            uint4 q = make_uint4(0, 0, 0, 0);
-            if (n * 8 + g < a.M && k < a.K) q = *reinterpret_cast<const uint4*>(a.x + (n * 8 + g) * a.ldx + k);
-            if constexpr (FMT == kFmtInt4) {
-              // the pairs that decode_int4 makes
-              x[n][b][0] = __byte_perm(q.x, q.z, 0x7632u);
-              x[n][b][1] = __byte_perm(q.x, q.z, 0x5410u);
-              x[n][b][2] = __byte_perm(q.y, q.w, 0x7632u);
-              x[n][b][3] = __byte_perm(q.y, q.w, 0x5410u);
-            } else {
-              x[n][b][0] = q.x, x[n][b][1] = q.y, x[n][b][2] = q.z, x[n][b][3] = q.w;
-            }
-          }
-      }
-      // scales (and zero points) of the chunk's groups, rows g and g + 8; zero past K
-      float s0[NB / GB + 1], s1[NB / GB + 1];
-      uint32_t z0[NB / GB + 1], z1[NB / GB + 1];
-      if constexpr (FMT != kFmtBf16) {
-#pragma unroll
-        for (int i = 0; i < NB / GB; ++i) {
-          const int grp = chunk * (NB / GB) + i;
-          const bool in = grp < a.groups;
-          const int64_t o0 = row0 * a.groups + (in ? grp : 0), o1 = row1 * a.groups + (in ? grp : 0);
-          if (a.scale_f32) {
-            s0[i] = in ? static_cast<const float*>(a.scales)[o0] : 0.0f;
-            s1[i] = in ? static_cast<const float*>(a.scales)[o1] : 0.0f;
-          } else {
-            s0[i] = in ? bf16_bits_to_float(static_cast<const uint16_t*>(a.scales)[o0]) : 0.0f;
-            s1[i] = in ? bf16_bits_to_float(static_cast<const uint16_t*>(a.scales)[o1]) : 0.0f;
-          }
-          if constexpr (FMT == kFmtInt4) {
-            const uint32_t q0 = a.zeros ? a.zeros[o0] & 15u : 8u, q1 = a.zeros ? a.zeros[o1] & 15u : 8u;
-            z0[i] = (q0 | 0x4300u) * 0x10001u;
-            z1[i] = (q1 | 0x4300u) * 0x10001u;
-          }
-        }
-      }
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      const unsigned char* piece = ring_p + stage * kPiece;
-      float c[NT][4];
+    for (int n = 0; n < NT; ++n) {
+      const uint16_t* src = x_lane + n * 8 * a.ldx + chunk * C::kChunkK;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        uint32_t v0[4], v1[4];  // rows g and g + 8
-        if constexpr (FMT == kFmtBf16) {
-          const uint32_t u = (static_cast<uint32_t>(b * 4 + t) ^ swz(g)) << 4;
-          const uint4 q0 = *reinterpret_cast<const uint4*>(piece + g * 128 + u);
-          const uint4 q1 = *reinterpret_cast<const uint4*>(piece + (g + 8) * 128 + u);
-          v0[0] = q0.x, v0[1] = q0.y, v0[2] = q0.z, v0[3] = q0.w;
-          v1[0] = q1.x, v1[1] = q1.y, v1[2] = q1.z, v1[3] = q1.w;
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (n * 8 + g < a.M && chunk * C::kChunkK + b * 32 + t * 8 < a.K) q = *reinterpret_cast<const uint4*>(src + b * 32);
+        if constexpr (FMT == kFmtInt4) {
+          // the pairs that decode_int4 makes
+          x[n][b][0] = __byte_perm(q.x, q.z, 0x7632u);
+          x[n][b][1] = __byte_perm(q.x, q.z, 0x5410u);
+          x[n][b][2] = __byte_perm(q.y, q.w, 0x7632u);
+          x[n][b][3] = __byte_perm(q.y, q.w, 0x5410u);
         } else {
-          const uint32_t u = ((static_cast<uint32_t>(b) ^ swz(g)) << 4) + t * 4;
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(piece + g * 128 + u);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(piece + (g + 8) * 128 + u);
-          if constexpr (FMT == kFmtInt4) {
-            decode_int4(w0, z0[b / GB], v0);
-            decode_int4(w1, z1[b / GB], v1);
-          } else {
-            decode_book(w0, book, v0);
-            decode_book(w1, book, v1);
+          x[n][b][0] = q.x, x[n][b][1] = q.y, x[n][b][2] = q.z, x[n][b][3] = q.w;
+        }
+      }
+    }
+  };
+  if (first < p.chunks) load_x(first);
+
+  const uint32_t lane_table = base + lane * 4;
+  if constexpr (FMT == kFmtCodebook) {
+    // Entry b: the pair of codes (b / 16, b % 16); thread b writes its 32 copies.
+    static_assert(kWarps * 32 == 256, "a thread per entry");
+    const float hi = codebook_entry(a.quant, threadIdx.x >> 4), lo = codebook_entry(a.quant, threadIdx.x & 15);
+    const uint32_t pair = pack_bf16x2(hi, lo);
+    const uint32_t rest = pack_bf16x2(hi - __uint_as_float(pair << 16), lo - __uint_as_float(pair & 0xffff0000u));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = (i + threadIdx.x) & 7;  // spread over the banks
+      reinterpret_cast<uint4*>(smem + threadIdx.x * 128)[q] = make_uint4(pair, pair, pair, pair);
+      if constexpr (TWO)
+        reinterpret_cast<uint4*>(smem + C::kTable + threadIdx.x * 128)[q] = make_uint4(rest, rest, rest, rest);
+    }
+    __syncthreads();
+  }
+
+  int stage = 0, buf = 0;
+  const uint32_t piece_lane = g * 128 + (FMT == kFmtBf16 ? 0 : t * 4);
+  for (int tile = cta; tile < p.tiles; tile += ctas, buf ^= 1) {
+    float acc[RT][NT][4] = {};
+    for (int chunk = first; chunk < p.chunks; chunk += stride) {
+      if (chunk != x_chunk) load_x(chunk);
+      float sc[RT][2][SPL];
+      uint32_t zz[RT][2][SPL];
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < SPL; ++i) {
+            sc[j][h][i] = ns[j][h][i];
+            zz[j][h][i] = nz[j][h][i];
           }
-          if constexpr (TWO) {
-            uint32_t r0[4], r1[4];
-            decode_book(w0, rest, r0);
-            decode_book(w1, rest, r1);
-            if (b % GB == 0)
+      if (chunk + stride < p.chunks) {
+        load_scales(chunk + stride);
+      } else if (tile + ctas < p.tiles) {
+        scale_rows(tile + ctas);
+        load_scales(first);
+      }
+      // Of group i of the chunk: row g (h = 0) or g + 8 of row tile j.
+      auto scale_of = [&](int j, int h, int i) { return __shfl_sync(0xffffffffu, sc[j][h][i % SPL], i / SPL, 4); };
+      auto zero_of = [&](int j, int h, int i) {
+        return (__shfl_sync(0xffffffffu, zz[j][h][i % SPL], i / SPL, 4) | 0x4300u) * 0x10001u;
+      };
+      cp_async_wait<KS - 2>();
+      __syncwarp();  // every lane's copies are in, and every lane is done with the stage filled next
+      put();
+      const uint32_t piece = ring + stage * C::kPiece + piece_lane;
+      float c[RT][NT][4];
+      uint32_t z[RT][2];
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
+      for (int b = 0; b < NB; ++b) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
+        for (int j = 0; j < RT; ++j) {
+          uint32_t v[2][4];  // rows g and g + 8
+          if (FMT != kFmtBf16 && b % GB == 0) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t m[4] = {r0[2 * h], r1[2 * h], r0[2 * h + 1], r1[2 * h + 1]};
-                mma16816(c[n], m, x[n][b][2 * h], x[n][b][2 * h + 1]);
-              }
+              for (int i = 0; i < 4; ++i) c[j][n][i] = 0.0f;
+            if constexpr (FMT == kFmtInt4)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) z[j][h] = zero_of(j, h, b / GB);
           }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float* d = FMT == kFmtBf16 ? acc[n] : c[n];
-          if (FMT != kFmtBf16 && !TWO && b % GB == 0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
+          uint32_t w[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t m[4] = {v0[2 * h], v1[2 * h], v0[2 * h + 1], v1[2 * h + 1]};
-            mma16816(d, m, x[n][b][2 * h], x[n][b][2 * h + 1]);
+            if constexpr (FMT == kFmtBf16) {
+              lds128(piece + j * 2048 + h * 1024 + ((static_cast<uint32_t>(b * 4 + t) ^ swz(g)) << 4), v[h]);
+            } else {
+              w[h] = lds32(piece + j * 2048 + h * 1024 + ((static_cast<uint32_t>(b) ^ swz(g)) << 4));
+              if constexpr (FMT == kFmtInt4)
+                decode_int4(w[h], z[j][h], v[h]);
+              else
+                decode_table(w[h], lane_table, v[h]);
+            }
+          }
+#pragma unroll
+          for (int two = 0; two < (TWO ? 2 : 1); ++two) {
+            if (two) {
+              decode_table(w[0], lane_table + C::kTable, v[0]);
+              decode_table(w[1], lane_table + C::kTable, v[1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t m[4] = {v[0][2 * i], v[1][2 * i], v[0][2 * i + 1], v[1][2 * i + 1]};
+                mma16816(FMT == kFmtBf16 ? acc[j][n] : c[j][n], m, x[n][b][2 * i], x[n][b][2 * i + 1]);
+              }
           }
           if (FMT != kFmtBf16 && b % GB == GB - 1) {
-            acc[n][0] = fmaf(s0[b / GB], c[n][0], acc[n][0]);
-            acc[n][1] = fmaf(s0[b / GB], c[n][1], acc[n][1]);
-            acc[n][2] = fmaf(s1[b / GB], c[n][2], acc[n][2]);
-            acc[n][3] = fmaf(s1[b / GB], c[n][3], acc[n][3]);
+            const float s0 = scale_of(j, 0, b / GB), s1 = scale_of(j, 1, b / GB);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              acc[j][n][0] = fmaf(s0, c[j][n][0], acc[j][n][0]);
+              acc[j][n][1] = fmaf(s0, c[j][n][1], acc[j][n][1]);
+              acc[j][n][2] = fmaf(s1, c[j][n][2], acc[j][n][2]);
+              acc[j][n][3] = fmaf(s1, c[j][n][3], acc[j][n][3]);
+            }
           }
         }
       }
-      __syncwarp();  // the stage that is filled next was read by all lanes
-      put();
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage = stage + 1 == KS ? 0 : stage + 1;
     }
     // Partial sums of the warps (and CTAs) that share rows, added in a fixed
     // order.  Two buffers: one barrier per tile.
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[buf][warp][n][i][lane] = acc[n][i];
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[buf][warp][j][n][i][lane] = acc[j][n][i];
     if (p.split > 1)
       cg::this_cluster().sync();
     else
       __syncthreads();
     if (rank == 0) {
-      const int ntok = a.M;
-      const int count = tile_out * ntok;
+      const int count = tile_out * a.M;
       for (int i = threadIdx.x; i < count; i += kWarps * 32) {
         const int o = i % tile_out, m = i / tile_out;
         const int col = tile * tile_out + o;
         if (col >= nout) continue;
-        const int w0 = (o / rows_out) * kw, r = o % rows_out;
+        const int w0 = (o / warp_out) * kw, j = (o % warp_out) / rows_out, r = o % rows_out;
         // MMA result i of lane (g, t): row g + 8 (i / 2), token 2 t + i % 2
         auto total = [&](int row) {
           float s = 0.0f;
           for (int q = 0; q < p.split; ++q) {
-            const float* base = &red[buf][w0][m >> 3][((row >> 3) << 1) | (m & 1)][((row & 7) << 2) | ((m & 7) >> 1)];
-            if (q) base = cg::this_cluster().map_shared_rank(base, cg::this_cluster().block_rank() + q);
-            for (int w = 0; w < kw; ++w) s += base[w * NT * 4 * 32];
+            const float* from = &red[buf][w0][j][m >> 3][((row >> 3) << 1) | (m & 1)][((row & 7) << 2) | ((m & 7) >> 1)];
+            if (q) from = cg::this_cluster().map_shared_rank(from, cg::this_cluster().block_rank() + q);
+            for (int w = 0; w < kw; ++w) s += from[w * RT * NT * 4 * 32];
           }
           return s;
         };
@@ -348,10 +396,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(Params p) {
   cp_async_wait<0>();
 }
 
-template <int FMT, int GB, int NT, bool TWO>
+template <int FMT, int GB, int NT, int RT, bool TWO>
 cudaError_t launch_one(const Params& p, int grid, cudaStream_t stream) {
-  constexpr size_t smem = kWarps * kStages * kPiece;
-  const void* f = reinterpret_cast<const void*>(gemv_kernel<FMT, GB, NT, TWO>);
+  constexpr size_t smem = Cfg<FMT, GB, NT, RT, TWO>::kSmem;
+  const void* f = reinterpret_cast<const void*>(gemv_kernel<FMT, GB, NT, RT, TWO>);
   if (cudaError_t err = ensure_smem_limit(f, smem); err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
@@ -365,17 +413,20 @@ cudaError_t launch_one(const Params& p, int grid, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
   LaunchScope ls(FMT == kFmtBf16 ? "gemv.bf16" : FMT == kFmtInt4 ? "gemv.int4" : "gemv.codebook", stream);
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<FMT, GB, NT, TWO>, p);
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<FMT, GB, NT, RT, TWO>, p);
+}
+
+template <int FMT, int GB, bool TWO>
+cudaError_t launch_rows(const Params& p, int rt, int grid, cudaStream_t stream) {
+  if (p.a.M > 8) return launch_one<FMT, GB, 2, 1, TWO>(p, grid, stream);
+  return rt == 2 ? launch_one<FMT, GB, 1, 2, TWO>(p, grid, stream) : launch_one<FMT, GB, 1, 1, TWO>(p, grid, stream);
 }
 
 template <int FMT, bool TWO>
-cudaError_t launch_group(const Params& p, int grid, cudaStream_t stream) {
-  const bool two_sets = p.a.M > 8;
-  if (p.a.group == 32)
-    return two_sets ? launch_one<FMT, 1, 2, TWO>(p, grid, stream) : launch_one<FMT, 1, 1, TWO>(p, grid, stream);
-  if (p.a.group == 64)
-    return two_sets ? launch_one<FMT, 2, 2, TWO>(p, grid, stream) : launch_one<FMT, 2, 1, TWO>(p, grid, stream);
-  return two_sets ? launch_one<FMT, 4, 2, TWO>(p, grid, stream) : launch_one<FMT, 4, 1, TWO>(p, grid, stream);
+cudaError_t launch_group(const Params& p, int rt, int grid, cudaStream_t stream) {
+  if (p.a.group == 32) return launch_rows<FMT, 1, TWO>(p, rt, grid, stream);
+  if (p.a.group == 64) return launch_rows<FMT, 2, TWO>(p, rt, grid, stream);
+  return launch_rows<FMT, 4, TWO>(p, rt, grid, stream);
 }
 
 }  // namespace
@@ -386,14 +437,18 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
   p.chunks = static_cast<int>((a.row_bytes + 127) / 128);
+  const int slots = 2 * di.sm_count;  // two CTAs fit an SM
   const int row_tiles = a.epi == kGemvNone ? (a.N + 15) / 16 : (a.N / 2 + 7) / 8;
-  // Two CTAs fit an SM.  The split of K over a CTA's warps that needs the fewest
-  // chunks in a row per warp, the widest of equals (its sums are ready first).
-  const int slots = 2 * di.sm_count;
+  // Two row tiles per warp share the tokens' registers; worth it once every warp
+  // of the GPU has several chunks anyway.
+  const int rt = a.M <= 8 && static_cast<int64_t>(row_tiles) * p.chunks >= 4ll * slots * kWarps ? 2 : 1;
+  // The split of K over a CTA's warps that needs the fewest steps: chunks of a
+  // warp's share, and about two for the sums that end a tile.
+  const int units = (row_tiles + rt - 1) / rt;
   int64_t best = -1;
   for (int kw = kWarps; kw >= 1; kw /= 2) {
-    const int64_t tiles = (row_tiles + kWarps / kw - 1) / (kWarps / kw);
-    const int64_t cost = (tiles + slots - 1) / slots * ((p.chunks + kw - 1) / kw);
+    const int64_t tiles = (units + kWarps / kw - 1) / (kWarps / kw);
+    const int64_t cost = (tiles + slots - 1) / slots * ((p.chunks + kw - 1) / kw * rt + 2);
     if (best < 0 || cost < best) {
       best = cost;
       p.kw = kw;
@@ -405,10 +460,10 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   p.split = 1;
   while (p.kw == kWarps && p.split < 8 && p.tiles * p.split * 2 <= slots && p.chunks >= kWarps * p.split * 2) p.split *= 2;
   const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, slots);
-  if (a.fmt == kGemvBf16)
-    return a.M > 8 ? launch_one<kFmtBf16, 1, 2, false>(p, grid, stream) : launch_one<kFmtBf16, 1, 1, false>(p, grid, stream);
-  if (a.fmt == kGemvInt4) return launch_group<kFmtInt4, false>(p, grid, stream);
-  return a.out_f32 ? launch_group<kFmtCodebook, true>(p, grid, stream) : launch_group<kFmtCodebook, false>(p, grid, stream);
+  if (a.fmt == kGemvBf16) return launch_rows<kFmtBf16, 1, false>(p, rt, grid, stream);
+  if (a.fmt == kGemvInt4) return launch_group<kFmtInt4, false>(p, rt, grid, stream);
+  return a.out_f32 ? launch_group<kFmtCodebook, true>(p, rt, grid, stream)
+                   : launch_group<kFmtCodebook, false>(p, rt, grid, stream);
 }
 
 }  // namespace e4b

@@ -568,11 +568,16 @@ _DTYPES = {torch.float32: E4B_F32, torch.bfloat16: E4B_BF16}
 def _launch(fn: str, device: torch.device, stream, *args) -> None:
     """Calls `fn` on the tensors' device: on `stream`, or on that device's current stream."""
     f = getattr(_lib or load_library(), fn)
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)  # what torch.cuda.current_stream(device) wraps
+    else:
+        stream = _stream(stream)
+    if index == torch._C._cuda_getDevice():
+        status = f(*args, stream)
+    else:
         with torch.cuda.device(device):
-            _check(f(*args, _stream(stream)), fn)
-        return
-    status = f(*args, _stream(stream))
+            status = f(*args, stream)
     if status != E4B_OK:
         _check(status, fn)
 
@@ -581,15 +586,19 @@ def _rows(t: Optional[torch.Tensor], name: str, M: int, H: int, device: torch.de
     """(pointer, dtype code, leading dimension) of a tensor of rows; (None, 0, 0) for None."""
     if t is None:
         return None, 0, 0
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != H or (H > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{M}, {H}] with unit column stride")
+    if t.shape != (M, H):
+        raise ValueError(f"{name} must be [{M}, {H}], got {list(t.shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and H > 1:
+        raise ValueError(f"{name} must have unit column stride")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    code = _DTYPES.get(t.dtype)
-    if code is None or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
+    own = t.dtype
+    code = _DTYPES.get(own)
+    if code is None or (dtype is not None and own != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {own}")
     # the stride of a single row says nothing
-    return t.data_ptr(), code, t.stride(0) if M > 1 else H
+    return t.data_ptr(), code, ld if M > 1 else H
 
 
 def _workspace_arg(workspace: Optional[torch.Tensor], device: torch.device):
@@ -663,23 +672,30 @@ def _gate(gate: Optional[torch.Tensor], M: int, H: int, device: torch.device):
     """(pointer, kind, dtype code) of a gate: [H] by channel, [M, 1] by token, [M, H] by element."""
     if gate is None:
         return None, E4B_GATE_NONE, 0
-    shape = tuple(gate.shape)
-    kind = {(H,): E4B_GATE_CHANNEL, (M, 1): E4B_GATE_TOKEN, (M, H): E4B_GATE_FULL}.get(shape)
-    if shape == (M, 1):
+    shape = gate.shape
+    if shape == (H,):
+        kind = E4B_GATE_CHANNEL
+    elif shape == (M, 1):
         kind = E4B_GATE_TOKEN
-    if kind is None or not gate.is_contiguous() or gate.dtype not in _DTYPES:
-        raise ValueError("gate must be [H], [M, 1] or [M, H], contiguous, in float32 or bfloat16")
+    elif shape == (M, H):
+        kind = E4B_GATE_FULL
+    else:
+        raise ValueError(f"gate must be [{H}], [{M}, 1] or [{M}, {H}], got {list(shape)}")
+    code = _DTYPES.get(gate.dtype)
+    if code is None or not gate.is_contiguous():
+        raise ValueError("gate must be contiguous, in float32 or bfloat16")
     if gate.device != device:
         raise ValueError(f"gate must be on {device}")
-    return gate.data_ptr(), kind, _DTYPES[gate.dtype]
+    return gate.data_ptr(), kind, code
 
 
 def _norm_device(t: torch.Tensor, norm: BlockNorm, name: str) -> torch.device:
-    if not t.is_cuda or t.dim() != 2:
+    device = t.device
+    if device.type != "cuda" or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    if norm.device is not None and norm.device != t.device:
+    if norm.device is not None and norm.device != device:
         raise ValueError(f"{name} must be on the weights' device, {norm.device}")
-    return t.device
+    return device
 
 
 def e4b_block_norm_forward(x: torch.Tensor, y: Optional[torch.Tensor], gate: Optional[torch.Tensor], norm: BlockNorm,
@@ -750,7 +766,7 @@ def _plain(t: Optional[torch.Tensor], name: str, shape, dtype, device: torch.dev
     """Pointer of a contiguous tensor of this shape, type and device; None for None."""
     if t is None:
         return None
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
     return t.data_ptr()
 
