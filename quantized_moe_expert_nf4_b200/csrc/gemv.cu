@@ -53,25 +53,27 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
   const int bytes = in ? 16 : 0;  // 0: writes zeros, reads nothing
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t v[4]) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
-}
-
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// As mma16816, from zero.
+__device__ __forceinline__ void mma16816_first(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // 16-byte unit `u` (0..7) of row `row` of a piece lies at unit u ^ swz(row): eight
@@ -85,21 +87,29 @@ __device__ __forceinline__ uint32_t swz(int row) { return ((row & 1) << 2) | ((r
 // Two integer instructions and one shared load per pair measured 2x faster in
 // the mainloop than byte permutes over the codebook in registers (21 integer
 // instructions per word, on a pipe of half the issue rate).
-__device__ __forceinline__ void decode_table(uint32_t w, uint32_t lane_table, uint32_t v[4]) {
-  v[0] = lds32(((w << 7) & 0x7f80u) + lane_table);
-  v[1] = lds32(((w >> 1) & 0x7f80u) + lane_table);
-  v[2] = lds32(((w >> 9) & 0x7f80u) + lane_table);
-  v[3] = lds32(((w >> 17) & 0x7f80u) + lane_table);
+__device__ __forceinline__ void decode_table(uint32_t w, const unsigned char* lane_table, uint32_t v[4]) {
+  v[0] = *reinterpret_cast<const uint32_t*>(lane_table + ((w << 7) & 0x7f80u));
+  v[1] = *reinterpret_cast<const uint32_t*>(lane_table + ((w >> 1) & 0x7f80u));
+  v[2] = *reinterpret_cast<const uint32_t*>(lane_table + ((w >> 9) & 0x7f80u));
+  v[3] = *reinterpret_cast<const uint32_t*>(lane_table + ((w >> 17) & 0x7f80u));
 }
 
 // Eight int4 codes -> bf16 pairs of elements (1, 5), (0, 4), (3, 7), (2, 6), each
 // 128 + code - (128 + zero); `zz` is bf16(128 + zero) in both halves.
-__device__ __forceinline__ void decode_int4(uint32_t w, uint32_t zz, uint32_t v[4]) {
+struct Int4Bits {
+  uint32_t mask, exponent;
+};
+__device__ __forceinline__ Int4Bits int4_bits() {
+  Int4Bits k;
+  asm volatile("mov.b32 %0, 0x000f000f;\n\tmov.b32 %1, 0x43004300;" : "=r"(k.mask), "=r"(k.exponent));
+  return k;
+}
+__device__ __forceinline__ void decode_int4(uint32_t w, uint32_t zz, const Int4Bits& k, uint32_t v[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t q = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q), *reinterpret_cast<const __nv_bfloat162*>(&zz));
-    v[i] = *reinterpret_cast<const uint32_t*>(&d);
+    uint32_t q;  // (w >> 4 i) & 0x000f000f | 0x43004300: one instruction once the constants sit in registers
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q) : "r"(w >> (4 * i)), "r"(k.mask), "r"(k.exponent));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(q), "r"(zz));
   }
 }
 
@@ -138,6 +148,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   const int warp_out = rows_out * RT, tile_out = warp_out * (kWarps / kw);
   const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   const uint32_t ring = base + C::kTables + warp * KS * C::kPiece;
+  const unsigned char* ring_p = smem + C::kTables + warp * KS * C::kPiece;
 
   // Row tile j of a tile: MMA rows 0..15 are weight rows o .. o + 15, or the gate
   // rows o .. o + 7 and the up rows half + o .. half + o + 7 of a gated product.
@@ -148,23 +159,31 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   int put_tile = cta, put_chunk = first, put_stage = 0, put_o = 0;
   const unsigned char* put_p = nullptr;
   const int64_t rb4 = a.row_bytes * 4, rb_up = static_cast<int64_t>(half) * a.row_bytes;
-  const uint32_t put_dst = (lane >> 3) * 128;
+  // Place of this lane's unit in rows lane / 8 and, 2 units over, lane / 8 + 4.
+  const uint32_t put_dst = (lane >> 3) * 128 + (((lane & 7) ^ swz(lane >> 3)) << 4);
+  bool put_whole = false;  // every row of the tile exists
   auto put_rows = [&]() {
-    put_o = put_tile * tile_out + wr * warp_out + (lane >> 3);
+    put_o = put_tile * tile_out + wr * warp_out;
+    put_whole = put_o + warp_out <= nout;
+    put_o += lane >> 3;
     put_p = static_cast<const unsigned char*>(a.w) + put_o * a.row_bytes + (lane & 7) * 16;
   };
   auto put = [&]() {
     if (put_tile < p.tiles && first < p.chunks) {
-      const int64_t off = static_cast<int64_t>(put_chunk) * 128;
-      const bool in_k = off + (lane & 7) * 16 < a.row_bytes;
-      const uint32_t dst = ring + put_stage * C::kPiece + put_dst;
+      const uint32_t dst = ring + put_stage * C::kPiece;
+      const unsigned char* src0 = put_p + static_cast<int64_t>(put_chunk) * 128;
+      auto src_of = [&](int i) { return src0 + (glu ? (i >> 2) * 2 + (i & 1) : i) * rb4 + (glu && (i & 2) ? rb_up : 0); };
+      auto dst_of = [&](int i) { return dst + (put_dst ^ ((i & 1) << 5)) + i * 512; };
+      if (put_whole && (put_chunk + 1) * 128ll <= a.row_bytes) {
 #pragma unroll
-      for (int i = 0; i < 4 * RT; ++i) {
-        // r: row within its row tile, less lane / 8
-        const int r = (i & 3) * 4, steps = glu ? (i >> 2) * 2 + (i & 1) : i;  // of 4 rows
-        const bool in = in_k && put_o + steps * 4 < nout;
-        const unsigned char* src = put_p + off + steps * rb4 + (glu && (i & 2) ? rb_up : 0);
-        cp_async16(dst + i * 512 + (((lane & 7) ^ swz(r + (lane >> 3))) << 4), in ? src : a.w, in);
+        for (int i = 0; i < 4 * RT; ++i) cp_async16(dst_of(i), src_of(i));
+      } else {
+        const bool in_k = put_chunk * 128ll + (lane & 7) * 16 < a.row_bytes;
+#pragma unroll
+        for (int i = 0; i < 4 * RT; ++i) {
+          const bool in = in_k && put_o + (glu ? (i >> 2) * 2 + (i & 1) : i) * 4 < nout;
+          cp_async16(dst_of(i), in ? src_of(i) : a.w, in);
+        }
       }
       put_chunk += stride;
       if (put_chunk >= p.chunks) {
@@ -185,7 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   // chunk's can be loaded while the one before it is multiplied.
   constexpr int SPL = NG > 4 ? NG / 4 : 1;
   float ns[RT][2][SPL];
-  uint32_t nz[RT][2][SPL];
+  uint32_t nz[RT][2][SPL] = {};
   int64_t s_row[RT][2];
   auto scale_rows = [&](int tile) {
 #pragma unroll
@@ -210,7 +229,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
             const float v = a.scale_f32 ? static_cast<const float*>(a.scales)[at]
                                         : bf16_bits_to_float(static_cast<const uint16_t*>(a.scales)[at]);
             ns[j][h][i] = in ? v : 0.0f;
-            if constexpr (FMT == kFmtInt4) nz[j][h][i] = a.zeros ? a.zeros[at] & 15u : 8u;
+            if constexpr (FMT == kFmtInt4)
+              if (a.zeros) nz[j][h][i] = a.zeros[at] & 15u;
           }
       }
     }
@@ -220,16 +240,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
 
   uint32_t x[NT][NB][4];
   int x_chunk = -1;
-  const uint16_t* x_lane = a.x + g * a.ldx + t * 8;
+  // Columns past the last token repeat it: their products are not written.
+  const uint16_t* x_lane[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) x_lane[n] = a.x + min(n * 8 + g, a.M - 1) * a.ldx + t * 8;
   auto load_x = [&](int chunk) {
     x_chunk = chunk;
+    const int k = chunk * C::kChunkK;
+    uint4 raw[NT][NB];
+    if (k + C::kChunkK <= a.K) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) raw[n][b] = *reinterpret_cast<const uint4*>(x_lane[n] + k + b * 32);
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          raw[n][b] = k + b * 32 + t * 8 < a.K ? *reinterpret_cast<const uint4*>(x_lane[n] + k + b * 32)
+                                               : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const uint16_t* src = x_lane + n * 8 * a.ldx + chunk * C::kChunkK;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (n * 8 + g < a.M && chunk * C::kChunkK + b * 32 + t * 8 < a.K) q = *reinterpret_cast<const uint4*>(src + b * 32);
+        const uint4 q = raw[n][b];
         if constexpr (FMT == kFmtInt4) {
           // the pairs that decode_int4 makes
           x[n][b][0] = __byte_perm(q.x, q.z, 0x7632u);
@@ -244,7 +280,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   };
   if (first < p.chunks) load_x(first);
 
-  const uint32_t lane_table = base + lane * 4;
+  const unsigned char* lane_table = smem + lane * 4;
+  const Int4Bits bits = int4_bits();
   if constexpr (FMT == kFmtCodebook) {
     // Entry b: the pair of codes (b / 16, b % 16); thread b writes its 32 copies.
     static_assert(kWarps * 32 == 256, "a thread per entry");
@@ -287,12 +324,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
       // Of group i of the chunk: row g (h = 0) or g + 8 of row tile j.
       auto scale_of = [&](int j, int h, int i) { return __shfl_sync(0xffffffffu, sc[j][h][i % SPL], i / SPL, 4); };
       auto zero_of = [&](int j, int h, int i) {
+        if (!a.zeros) return 0x43084308u;
         return (__shfl_sync(0xffffffffu, zz[j][h][i % SPL], i / SPL, 4) | 0x4300u) * 0x10001u;
       };
       cp_async_wait<KS - 2>();
       __syncwarp();  // every lane's copies are in, and every lane is done with the stage filled next
       put();
-      const uint32_t piece = ring + stage * C::kPiece + piece_lane;
+      const unsigned char* piece = ring_p + stage * C::kPiece + piece_lane;
       float c[RT][NT][4];
       uint32_t z[RT][2];
 #pragma unroll
@@ -300,24 +338,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
           uint32_t v[2][4];  // rows g and g + 8
-          if (FMT != kFmtBf16 && b % GB == 0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) c[j][n][i] = 0.0f;
-            if constexpr (FMT == kFmtInt4)
+          if constexpr (FMT == kFmtInt4)
+            if (b % GB == 0)
 #pragma unroll
               for (int h = 0; h < 2; ++h) z[j][h] = zero_of(j, h, b / GB);
-          }
           uint32_t w[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if constexpr (FMT == kFmtBf16) {
-              lds128(piece + j * 2048 + h * 1024 + ((static_cast<uint32_t>(b * 4 + t) ^ swz(g)) << 4), v[h]);
+              const uint4 q = *reinterpret_cast<const uint4*>(piece + j * 2048 + h * 1024 +
+                                                              ((static_cast<uint32_t>(b * 4 + t) ^ swz(g)) << 4));
+              v[h][0] = q.x, v[h][1] = q.y, v[h][2] = q.z, v[h][3] = q.w;
             } else {
-              w[h] = lds32(piece + j * 2048 + h * 1024 + ((static_cast<uint32_t>(b) ^ swz(g)) << 4));
+              w[h] = *reinterpret_cast<const uint32_t*>(piece + j * 2048 + h * 1024 +
+                                                        ((static_cast<uint32_t>(b) ^ swz(g)) << 4));
               if constexpr (FMT == kFmtInt4)
-                decode_int4(w[h], z[j][h], v[h]);
+                decode_int4(w[h], z[j][h], bits, v[h]);
               else
                 decode_table(w[h], lane_table, v[h]);
             }
@@ -333,7 +369,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const uint32_t m[4] = {v[0][2 * i], v[1][2 * i], v[0][2 * i + 1], v[1][2 * i + 1]};
-                mma16816(FMT == kFmtBf16 ? acc[j][n] : c[j][n], m, x[n][b][2 * i], x[n][b][2 * i + 1]);
+                if (FMT != kFmtBf16 && b % GB == 0 && two == 0 && i == 0)
+                  mma16816_first(c[j][n], m, x[n][b][2 * i], x[n][b][2 * i + 1]);
+                else
+                  mma16816(FMT == kFmtBf16 ? acc[j][n] : c[j][n], m, x[n][b][2 * i], x[n][b][2 * i + 1]);
               }
           }
           if (FMT != kFmtBf16 && b % GB == GB - 1) {
