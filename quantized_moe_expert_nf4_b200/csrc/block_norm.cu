@@ -6,10 +6,14 @@
 //   n = N(r; w_next)
 //   N(v; w) = v * rstd(v) * (w + offset),  rstd(v) = 1 / sqrt(mean(v^2) + eps)
 //
-// Bound: HBM.  A row is read once into registers, both norms are taken on the
-// 32-bit values there (n from the unrounded r), and every output is rounded
-// once.  T threads share a row, each with VPT vectors of 8 columns: a row's
-// sum of squares is a warp shuffle and, above one warp, one block barrier.
+// Bound: HBM.  CTAs are persistent and take a row at a time; T threads share
+// it, each with VPT groups of 8 columns.  The rows ahead come through a ring of
+// cp.async stages in shared memory, so that loads stay in flight while a row's
+// sums meet (a warp shuffle and a block barrier per sum).  Where rows can be
+// moved as vectors, a thread copies and reads its own columns only; other rows
+// (odd widths, strides) are copied as the 16-byte units that they touch and
+// read by element.  Both norms are taken on 32-bit values in registers (n from the
+// unrounded r), and every output is rounded once.
 //
 // Backward, with d = dr + (dn through the next norm):
 //   h = dn * (w_next + offset):  d += rstd_r * (h - rhat * mean(h * rhat))
@@ -17,9 +21,9 @@
 //   k = dz * (w_post + offset):  dy = rstd_y * (k - yhat * mean(k * yhat))
 //   dw_next = sum_m dn * rhat,  dw_post = sum_m dz * yhat
 // Both rstd are taken again from r and y, which the gradients need anyway, so
-// the forward saves nothing.  The CTAs are persistent and keep their columns'
-// sums over rows in registers; a second kernel adds the CTAs' partial sums in
-// CTA order, so every sum has a fixed order.
+// the forward saves nothing.  A CTA keeps its columns' sums over rows in
+// registers; a second kernel adds the CTAs' partial sums in CTA order, so every
+// sum has a fixed order.
 #include <algorithm>
 #include <string>
 
@@ -32,16 +36,26 @@ namespace {
 constexpr int kMaxNormH = 16384;
 constexpr int kMaxNormThreads = 512;
 
+// A tensor of rows that a kernel reads: leading dimension in elements, place in a
+// ring stage.
+struct RowSrc {
+  const void* p;
+  int64_t ld;
+  uint32_t off;
+};
+
 struct NormArgs {
-  const void *x, *y, *gate, *w_post, *w_next;
-  const void *dr, *dn;               // backward
+  RowSrc x, y, gate;                 // x: also r of the backward; gate: E4B_GATE_FULL's rows
+  RowSrc dr, dn;                     // backward
+  const void *vec_gate, *w_post, *w_next;  // vec_gate: channel or token gate
   void *r, *n;                       // forward
   void *dx, *dy, *dgate;             // backward
   float* partial;                    // backward: [3][parts][H] column sums (w_post, w_next, channel gate)
-  int64_t ldx, ldy, ldr, ldn;        // ldx also of dr and dx, ldy of dy, ldn of dn
-  int64_t lddr, lddx, lddy;
+  int64_t ldr, ldn, lddx, lddy;      // of the outputs
   int64_t M;
   int H, parts;
+  int stages;                        // of the ring; 0: rows are read from memory directly
+  uint32_t stage_bytes;
   int gate_kind, gate_f32, sigmoid, w_f32, n_f32;
   float scale, offset, eps, inv_h;
 };
@@ -64,18 +78,39 @@ __device__ __forceinline__ void load8(const uint16_t* p, float v[8]) {
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
+// One 32-byte store: two of 16 bytes would each write half of every sector.
 __device__ __forceinline__ void store8(float* p, const float v[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float v[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                             pack_bf16x2(v[6], v[7]));
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cp16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+// Through L1: the two halves of a 32-byte sector are asked for by two instructions.
+__device__ __forceinline__ void cp16_l1(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the newest stages - 2 groups are in (stages is 2 to 4).
+__device__ __forceinline__ void cp_wait(int stages) {
+  if (stages == 4)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (stages == 3)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // One thread's share of a row: VPT groups of 8 columns.  VEC: a group is 8
-// adjacent columns, moved as 16-byte vectors; otherwise (odd widths, strides
-// or bases) its columns lie T apart, so that a warp's accesses stay adjacent.
+// adjacent columns, moved as vectors; otherwise its columns lie T apart, so
+// that a warp's accesses stay adjacent.
 template <bool VEC>
 struct Cols {
   int T, t, H;
@@ -117,195 +152,298 @@ struct Cols {
     else
       store(static_cast<uint16_t*>(base) + off, v, in);
   }
+
+  // Row m of `s` into its place in `stage`.
+  template <class E>
+  __device__ __forceinline__ void fetch(unsigned char* stage, const RowSrc& s, int64_t m, int64_t M, int VPT) const {
+    const E* row = static_cast<const E*>(s.p) + m * s.ld;
+    unsigned char* dst = stage + s.off;
+    if constexpr (VEC) {
+      // 8 bf16: one unit per thread; 8 floats: two, in two planes
+      for (int v = 0; v < VPT; ++v) {
+        if (col(v, 0) >= H) break;
+        if constexpr (sizeof(E) == 2) {
+          cp16(dst + (v * T + t) * 16, row + col(v, 0), 16);
+        } else {
+          cp16_l1(dst + (v * T + t) * 16, row + col(v, 0));
+          cp16_l1(dst + ((VPT + v) * T + t) * 16, row + col(v, 0) + 4);
+        }
+      }
+    } else {
+      // the 16-byte units that the row touches: its neighbours' ends come along,
+      // but nothing past the last row's end
+      const uintptr_t at = reinterpret_cast<uintptr_t>(row), lead = at & 15;
+      const uintptr_t end = at + ((M - 1 - m) * s.ld + H) * sizeof(E);
+      const int bytes = static_cast<int>(lead) + H * static_cast<int>(sizeof(E));
+      for (int u = t; u * 16 < bytes; u += T) {
+        const uintptr_t from = at - lead + u * 16;
+        cp16(dst + u * 16, reinterpret_cast<const void*>(from), end - from < 16 ? static_cast<int>(end - from) : 16);
+      }
+    }
+  }
+  // Group v of row m, from the stage that fetch() filled.
+  template <class E>
+  __device__ __forceinline__ void staged(const unsigned char* stage, const RowSrc& s, int64_t m, int v, int VPT,
+                                         float out[8]) const {
+    const unsigned char* src = stage + s.off;
+    if constexpr (VEC) {
+      if (col(v, 0) >= H) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = 0.0f;
+        return;
+      }
+      if constexpr (sizeof(E) == 2) {
+        load8(reinterpret_cast<const uint16_t*>(src + (v * T + t) * 16), out);
+      } else {
+        const float4 lo = *reinterpret_cast<const float4*>(src + (v * T + t) * 16);
+        const float4 hi = *reinterpret_cast<const float4*>(src + ((VPT + v) * T + t) * 16);
+        out[0] = lo.x, out[1] = lo.y, out[2] = lo.z, out[3] = lo.w, out[4] = hi.x, out[5] = hi.y, out[6] = hi.z, out[7] = hi.w;
+      }
+    } else {
+      const uintptr_t lead = reinterpret_cast<uintptr_t>(static_cast<const E*>(s.p) + m * s.ld) & 15;
+      load(reinterpret_cast<const E*>(src + lead), v, out);
+    }
+  }
 };
 
 __device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-// Sums of NV values over the T threads of a row (T a multiple of 32; every
-// thread of the block calls this).  `red` holds NV floats per warp of the
-// block.  One barrier: a caller that sums again passes another buffer.
+// The rows of a CTA, one after another.
+template <class XT, class YT, int VPT, bool VEC, bool BWD>
+struct Rows {
+  const NormArgs& a;
+  const Cols<VEC>& c;
+  unsigned char* ring;
+  int put_stage = 0, stage = 0;
+  int64_t put_row, step;
+
+  __device__ __forceinline__ Rows(const NormArgs& a_, const Cols<VEC>& c_, unsigned char* ring_)
+      : a(a_), c(c_), ring(ring_), put_row(blockIdx.x), step(gridDim.x) {
+    for (int i = 0; i + 1 < a.stages; ++i) put();
+  }
+  __device__ __forceinline__ void put() {
+    if (put_row < a.M) {
+      unsigned char* to = ring + put_stage * a.stage_bytes;
+      if constexpr (BWD) {
+        if (a.dr.p) c.template fetch<XT>(to, a.dr, put_row, a.M, VPT);
+        if (a.w_next) {
+          c.template fetch<XT>(to, a.x, put_row, a.M, VPT);
+          a.n_f32 ? c.template fetch<float>(to, a.dn, put_row, a.M, VPT) : c.template fetch<uint16_t>(to, a.dn, put_row, a.M, VPT);
+        }
+      } else {
+        c.template fetch<XT>(to, a.x, put_row, a.M, VPT);
+      }
+      if (a.y.p) c.template fetch<YT>(to, a.y, put_row, a.M, VPT);
+      if (a.gate.p)
+        a.gate_f32 ? c.template fetch<float>(to, a.gate, put_row, a.M, VPT) : c.template fetch<uint16_t>(to, a.gate, put_row, a.M, VPT);
+      put_row += step;
+    }
+    cp_commit();
+    put_stage = put_stage + 1 == a.stages ? 0 : put_stage + 1;
+  }
+  // Makes the next row readable and sets the row `stages - 1` further off.  The
+  // stage that it fills is the last row's: this thread's own part of it, or,
+  // read across threads, behind a barrier that they all reach after it.
+  __device__ __forceinline__ void next() {
+    if (!a.stages) return;
+    cp_wait(a.stages);
+    if constexpr (!VEC) __syncthreads();
+    put();
+  }
+  __device__ __forceinline__ void done() {
+    if (a.stages) stage = stage + 1 == a.stages ? 0 : stage + 1;
+  }
+  template <class E>
+  __device__ __forceinline__ void load(const RowSrc& s, int64_t m, int v, float out[8]) const {
+    if (a.stages)
+      c.template staged<E>(ring + stage * a.stage_bytes, s, m, v, VPT, out);
+    else
+      c.load(static_cast<const E*>(s.p) + m * s.ld, v, out);
+  }
+  __device__ __forceinline__ void load(const RowSrc& s, int64_t m, int f32, int v, float out[8]) const {
+    if (f32)
+      load<float>(s, m, v, out);
+    else
+      load<uint16_t>(s, m, v, out);
+  }
+  // Factor f of the gate for a group of columns; with `slope`, also df/dgate.
+  __device__ __forceinline__ void factor(int64_t m, int v, float f[8], float* slope) const {
+    if (a.gate_kind == E4B_GATE_NONE) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+      return;
+    }
+    if (a.gate_kind == E4B_GATE_TOKEN) {
+      const float g = a.gate_f32 ? load1(static_cast<const float*>(a.vec_gate) + m)
+                                 : load1(static_cast<const uint16_t*>(a.vec_gate) + m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = g;
+    } else if (a.gate_kind == E4B_GATE_CHANNEL) {
+      c.load(a.vec_gate, 0, a.gate_f32, v, f);
+    } else {
+      load(a.gate, m, a.gate_f32, v, f);
+    }
+    if (a.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = sigmoid_f32(f[j]);
+    }
+    if (slope) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) slope[j] = a.sigmoid ? f[j] * (1.0f - f[j]) : 1.0f;
+    }
+  }
+};
+
+
+// Sums of up to three values over the CTA's T threads (a multiple of 32).  One
+// barrier above one warp: a caller that sums again passes another buffer.
 template <int NV>
-__device__ __forceinline__ void row_sum(float v[NV], int T, float* red) {
+__device__ __forceinline__ void row_sum(float v[NV], int T, float4* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if (T == 32) return;
-  const int warps = T >> 5;
-  float* mine = red + threadIdx.y * warps * NV;
   if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) mine[(threadIdx.x >> 5) * NV + i] = v[i];
+    red[threadIdx.x >> 5] = make_float4(v[0], NV > 1 ? v[NV > 1 ? 1 : 0] : 0.0f, NV > 2 ? v[NV > 2 ? 2 : 0] : 0.0f, 0.0f);
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = 0.0f;
-  for (int w = 0; w < warps; ++w)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += mine[w * NV + i];
+  for (int w = 0; w < T >> 5; ++w) {
+    const float4 q = red[w];
+    v[0] += q.x;
+    if (NV > 1) v[NV > 1 ? 1 : 0] += q.y;
+    if (NV > 2) v[NV > 2 ? 2 : 0] += q.z;
+  }
 }
 
-// Factor f of the gate for one group of columns; with `slope`, also df/dgate.
-template <bool VEC>
-__device__ __forceinline__ void gate_factor(const NormArgs& a, const Cols<VEC>& c, int64_t m, int v, float f[8],
-                                            float* slope) {
-  if (a.gate_kind == E4B_GATE_NONE) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 1.0f;
-    return;
-  }
-  if (a.gate_kind == E4B_GATE_TOKEN) {
-    float g = 0.0f;
-    if (c.H > 0)  // a row past the last one reads nothing
-      g = a.gate_f32 ? load1(static_cast<const float*>(a.gate) + m) : load1(static_cast<const uint16_t*>(a.gate) + m);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = g;
-  } else {
-    c.load(a.gate, a.gate_kind == E4B_GATE_FULL ? m * a.H : 0, a.gate_f32, v, f);
-  }
-  if (a.sigmoid) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = sigmoid_f32(f[j]);
-  }
-  if (slope) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) slope[j] = a.sigmoid ? f[j] * (1.0f - f[j]) : 1.0f;
-  }
-}
+// Most threads of a CTA, and CTAs an SM should hold, by the groups of a thread.
+constexpr int norm_threads(int vpt) { return vpt == 4 ? 512 : 384; }
 
 template <class XT, class YT, int VPT, bool VEC>
-__global__ void __launch_bounds__(kMaxNormThreads) block_norm_forward_kernel(NormArgs a) {
-  __shared__ float red[2][kMaxNormThreads / 32];
+__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2 : 1) block_norm_forward_kernel(NormArgs a) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  // Buffers alternate by row: a row may have one sum only, and so no other
+  // barrier before the next row's.
+  __shared__ float4 red[2][2][kMaxNormThreads / 32];
   const int T = blockDim.x;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const bool live = m < a.M;
-  const Cols<VEC> c{T, static_cast<int>(threadIdx.x), live ? a.H : 0};
-  float r[VPT][8], z[VPT][8];
-  const XT* x = static_cast<const XT*>(a.x) + m * a.ldx;
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) c.load(x, v, r[v]);
-  if (a.y) {
-    const YT* y = static_cast<const YT*>(a.y) + m * a.ldy;
-    float ss[1] = {0.0f};
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      c.load(y, v, z[v]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] += z[v][j] * z[v][j];
-    }
-    float rstd = 1.0f;
-    if (a.w_post) {
-      row_sum<1>(ss, T, red[0]);
-      rstd = rsqrtf(ss[0] * a.inv_h + a.eps);
-    }
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      float f[8];
-      gate_factor(a, c, m, v, f, nullptr);
-      if (a.w_post) {
-        float w[8];
-        c.load(a.w_post, 0, a.w_f32, v, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[v][j] *= rstd * (w[j] + a.offset);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[v][j] = fmaf(a.scale * f[j], z[v][j], r[v][j]);
-      c.store(static_cast<XT*>(a.r) + m * a.ldr, v, r[v]);
-    }
-  }
-  if (!a.w_next) return;
-  float ss[1] = {0.0f};
-#pragma unroll
-  for (int v = 0; v < VPT; ++v)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c.col(v, j) < c.H) ss[0] += r[v][j] * r[v][j];
-  row_sum<1>(ss, T, red[1]);
-  const float rstd = rsqrtf(ss[0] * a.inv_h + a.eps);
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    float w[8];
-    c.load(a.w_next, 0, a.w_f32, v, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = r[v][j] * rstd * (w[j] + a.offset);
-    c.store(a.n, m * a.ldn, a.n_f32, v, w);
-  }
-}
-
-template <class XT, class YT, int VPT, bool VEC>
-__global__ void __launch_bounds__(kMaxNormThreads) block_norm_backward_kernel(NormArgs a) {
-  // The first sum of a row alternates between two buffers: there may be no
-  // second sum, and so no other barrier, before the next row's.
-  __shared__ float red[3][3 * kMaxNormThreads / 32];
+  const Cols<VEC> c{T, static_cast<int>(threadIdx.x), a.H};
+  Rows<XT, YT, VPT, VEC, false> rows(a, c, ring);
   int odd = 0;
-  const int T = blockDim.x;
-  const Cols<VEC> all{T, static_cast<int>(threadIdx.x), a.H};
-  float s_post[VPT][8] = {}, s_next[VPT][8] = {}, s_gate[VPT][8] = {};
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
-  // All rows of a block go through the loop together (row_sum has a barrier).
-  for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; m0 < a.M; m0 += step) {
-    const int64_t m = m0 + threadIdx.y;
-    const bool live = m < a.M;
-    const Cols<VEC> c{T, static_cast<int>(threadIdx.x), live ? a.H : 0};
-    float d[VPT][8], r[VPT][8], h[VPT][8], y[VPT][8];
-    float s1[3] = {0.0f, 0.0f, 0.0f};  // sum r^2, sum h * r, sum y^2
-    const XT* dr = static_cast<const XT*>(a.dr) + m * a.lddr;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, odd ^= 1, rows.done()) {
+    rows.next();
+    float r[VPT][8], z[VPT][8];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      if (a.dr) {
-        c.load(dr, v, d[v]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[v][j] = 0.0f;
-      }
-      if (a.y) c.load(static_cast<const YT*>(a.y) + m * a.ldy, v, y[v]);
-      if (a.w_next) {
-        c.load(static_cast<const XT*>(a.r) + m * a.ldr, v, r[v]);
-        c.load(a.dn, m * a.ldn, a.n_f32, v, h[v]);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      if (a.y) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s1[2] += y[v][j] * y[v][j];
-      }
-      if (a.w_next) {
-        float w[8];
-        c.load(a.w_next, 0, a.w_f32, v, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s1[0] += r[v][j] * r[v][j];
-          s1[1] += h[v][j] * (w[j] + a.offset) * r[v][j];
-        }
-      }
-    }
-    row_sum<3>(s1, T, red[odd]);
-    odd ^= 1;
-    if (a.w_next) {
-      const float rstd = rsqrtf(s1[0] * a.inv_h + a.eps);
-      const float mean = s1[1] * rstd * a.inv_h;  // mean(h * rhat)
+    for (int v = 0; v < VPT; ++v) rows.template load<XT>(a.x, m, v, r[v]);
+    if (a.y.p) {
+      float ss[1] = {0.0f};
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        float w[8];
+        rows.template load<YT>(a.y, m, v, z[v]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss[0] += z[v][j] * z[v][j];
+      }
+      float rstd = 1.0f;
+      if (a.w_post) {
+        row_sum<1>(ss, T, red[odd][0]);
+        rstd = rsqrtf(ss[0] * a.inv_h + a.eps);
+      }
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        float f[8];
+        rows.factor(m, v, f, nullptr);
+        if (a.w_post) {
+          float w[8];
+          c.load(a.w_post, 0, a.w_f32, v, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[v][j] *= rstd * (w[j] + a.offset);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[v][j] = fmaf(a.scale * f[j], z[v][j], r[v][j]);
+        c.store(static_cast<XT*>(a.r) + m * a.ldr, v, r[v]);
+      }
+    }
+    if (!a.w_next) continue;
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss[0] += c.col(v, j) < c.H ? r[v][j] * r[v][j] : 0.0f;
+    row_sum<1>(ss, T, red[odd][1]);
+    const float rstd = rsqrtf(ss[0] * a.inv_h + a.eps);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float w[8];
+      c.load(a.w_next, 0, a.w_f32, v, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = r[v][j] * rstd * (w[j] + a.offset);
+      c.store(a.n, m * a.ldn, a.n_f32, v, w);
+    }
+  }
+}
+
+template <class XT, class YT, int VPT, bool VEC>
+__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1) block_norm_backward_kernel(NormArgs a) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float4 red[2][2][kMaxNormThreads / 32];  // as in the forward
+  const int T = blockDim.x;
+  const Cols<VEC> c{T, static_cast<int>(threadIdx.x), a.H};
+  Rows<XT, YT, VPT, VEC, true> rows(a, c, ring);
+  float s_post[VPT][8] = {}, s_next[VPT][8] = {}, s_gate[VPT][8] = {};
+  int odd = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, odd ^= 1, rows.done()) {
+    rows.next();
+    float s1[3] = {0.0f, 0.0f, 0.0f};  // sum r^2, sum h * r, sum y^2
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float p[8], q[8], w[8];
+      if (a.y.p) {
+        rows.template load<YT>(a.y, m, v, p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s1[2] += p[j] * p[j];
+      }
+      if (a.w_next) {
+        rows.template load<XT>(a.x, m, v, p);
+        rows.load(a.dn, m, a.n_f32, v, q);
         c.load(a.w_next, 0, a.w_f32, v, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float hat = r[v][j] * rstd;
-          s_next[v][j] += h[v][j] * hat;
-          d[v][j] += rstd * (h[v][j] * (w[j] + a.offset) - hat * mean);
+          s1[0] += p[j] * p[j];
+          s1[1] += q[j] * (w[j] + a.offset) * p[j];
         }
       }
     }
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-      if (a.dx) c.store(static_cast<XT*>(a.dx) + m * a.lddx, v, d[v]);
-    if (!a.y) continue;
-    const float rstd = a.w_post ? rsqrtf(s1[2] * a.inv_h + a.eps) : 1.0f;
+    row_sum<3>(s1, T, red[odd][0]);
+    const float rstd_r = rsqrtf(s1[0] * a.inv_h + a.eps), rstd_y = a.w_post ? rsqrtf(s1[2] * a.inv_h + a.eps) : 1.0f;
+    const float mean_r = s1[1] * rstd_r * a.inv_h;  // mean(h * rhat)
+    float k[VPT][8];
     float s2[2] = {0.0f, 0.0f};  // sum k * yhat, sum d * z * slope
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      float f[8], slope[8], w[8];
-      gate_factor(a, c, m, v, f, slope);
+      float* d = k[v];
+      if (a.dr.p) {
+        rows.template load<XT>(a.dr, m, v, d);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = 0.0f;
+      }
+      if (a.w_next) {
+        float p[8], q[8], w[8];
+        rows.template load<XT>(a.x, m, v, p);
+        rows.load(a.dn, m, a.n_f32, v, q);
+        c.load(a.w_next, 0, a.w_f32, v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float hat = p[j] * rstd_r;
+          s_next[v][j] += q[j] * hat;
+          d[j] += rstd_r * (q[j] * (w[j] + a.offset) - hat * mean_r);
+        }
+      }
+      if (a.dx) c.store(static_cast<XT*>(a.dx) + m * a.lddx, v, d);
+      if (!a.y.p) continue;
+      float y[8], f[8], slope[8], w[8];
+      rows.template load<YT>(a.y, m, v, y);
+      rows.factor(m, v, f, slope);
       if (a.w_post) {
         c.load(a.w_post, 0, a.w_f32, v, w);
 #pragma unroll
@@ -317,50 +455,54 @@ __global__ void __launch_bounds__(kMaxNormThreads) block_norm_backward_kernel(No
       float dg[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float hat = y[v][j] * rstd, ds = a.scale * d[v][j];
+        const float hat = y[j] * rstd_y, ds = a.scale * d[j];
         const float dz = ds * f[j];
         if (a.gate_kind != E4B_GATE_NONE) dg[j] = ds * hat * w[j] * slope[j];
         if (a.gate_kind == E4B_GATE_CHANNEL) s_gate[v][j] += dg[j];
         if (a.gate_kind == E4B_GATE_TOKEN) s2[1] += dg[j];
         s_post[v][j] += dz * hat;
-        d[v][j] = dz * w[j];  // k
-        s2[0] += d[v][j] * hat;
+        d[j] = dz * w[j];
+        s2[0] += d[j] * hat;
       }
       if (a.gate_kind == E4B_GATE_FULL && a.dgate) c.store(a.dgate, m * a.H, a.gate_f32, v, dg);
     }
-    if (a.w_post || a.gate_kind == E4B_GATE_TOKEN) row_sum<2>(s2, T, red[2]);
-    if (a.gate_kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0 && live) {
+    if (!a.y.p) continue;
+    if (a.w_post || a.gate_kind == E4B_GATE_TOKEN) row_sum<2>(s2, T, red[odd][1]);
+    if (a.gate_kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0) {
       if (a.gate_f32)
         store1(static_cast<float*>(a.dgate) + m, s2[1]);
       else
         store1(static_cast<uint16_t*>(a.dgate) + m, s2[1]);
     }
-    const float mean = a.w_post ? s2[0] * a.inv_h : 0.0f;
+    if (!a.dy) continue;
+    const float mean_y = a.w_post ? s2[0] * a.inv_h : 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      float o[8];
+      float y[8];
+      rows.template load<YT>(a.y, m, v, y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = rstd * (d[v][j] - y[v][j] * rstd * mean);
-      if (a.dy) c.store(static_cast<YT*>(a.dy) + m * a.lddy, v, o);
+      for (int j = 0; j < 8; ++j) y[j] = rstd_y * (k[v][j] - y[j] * rstd_y * mean_y);
+      c.store(static_cast<YT*>(a.dy) + m * a.lddy, v, y);
     }
   }
-  const int64_t part = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y, plane = static_cast<int64_t>(a.parts) * a.H;
+  const int64_t plane = static_cast<int64_t>(a.parts) * a.H;
+  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.H;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    if (a.w_post) all.store(a.partial + part * a.H, v, s_post[v]);
-    if (a.w_next) all.store(a.partial + plane + part * a.H, v, s_next[v]);
-    if (a.gate_kind == E4B_GATE_CHANNEL) all.store(a.partial + 2 * plane + part * a.H, v, s_gate[v]);
+    if (a.w_post) c.store(part, v, s_post[v]);
+    if (a.w_next) c.store(part + plane, v, s_next[v]);
+    if (a.gate_kind == E4B_GATE_CHANNEL) c.store(part + 2 * plane, v, s_gate[v]);
   }
 }
 
-// out[q][col] = sum over parts of partial[q][part][col], in a fixed order: 8
-// threads of a column take every 8th part, then are added in order.
+// out[q][col] = sum over parts of partial[q][part][col], in a fixed order: 16
+// threads of a column take every 16th part, then are added in order.
 struct ReduceArgs {
   const float* partial;
   float* out[3];
   int parts, H;
 };
-constexpr int kRedCols = 32, kRedLanes = 8;
+constexpr int kRedCols = 32, kRedLanes = 16;
 
 __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel(ReduceArgs a) {
   float* out = a.out[blockIdx.y];
@@ -370,6 +512,7 @@ __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel
   float sum = 0.0f;
   if (col < a.H) {
     const float* p = a.partial + static_cast<int64_t>(blockIdx.y) * a.parts * a.H + col;
+#pragma unroll 4
     for (int i = threadIdx.y; i < a.parts; i += kRedLanes) sum += p[static_cast<int64_t>(i) * a.H];
   }
   s[threadIdx.y][threadIdx.x] = sum;
@@ -381,67 +524,86 @@ __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel
 }
 
 struct NormShape {
-  int T, rows, vpt;
+  int T, vpt, grid;
 };
 
-NormShape norm_shape(int H, int vpt_max) {
+constexpr int kSms = 148;
+
+// Threads of a row, their groups, and the persistent CTAs.  The workspace query
+// and the launch agree because both go by M and H alone.
+NormShape norm_shape(int64_t M, int H, int threads_per_sm) {
   const int nvec = (H + 7) / 8;
   NormShape s{};
-  s.vpt = 1;
-  while (s.vpt < 4 && (s.vpt < vpt_max ? nvec > 32 * s.vpt : nvec > kMaxNormThreads * s.vpt)) s.vpt *= 2;
+  s.vpt = nvec <= norm_threads(1) ? 1 : nvec <= 2 * norm_threads(2) ? 2 : 4;
   s.T = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
-  s.rows = s.T >= 128 ? 1 : 128 / s.T;
+  const int per_sm = std::min(16, std::max(1, threads_per_sm / s.T));
+  s.grid = static_cast<int>(std::min<int64_t>(M, kSms * per_sm));
   return s;
 }
+constexpr int kForwardThreads = 1152, kBackwardThreads = 768;  // per SM
 
-// Persistent CTAs of the backward, 768 threads on each of the B200's 148 SMs,
-// and the partial sums they leave: one for each row slot of a CTA.
-int backward_parts(int64_t M, const NormShape& s, int* grid) {
-  const int64_t blocks = (M + s.rows - 1) / s.rows;
-  const int per_sm = std::max(1, 768 / (s.T * s.rows));
-  *grid = static_cast<int>(std::min<int64_t>(blocks, 148 * per_sm));
-  return *grid * s.rows;
+// The ring: as many stages (2 to 4) as leave room for the SM's other CTAs, or, of
+// rows too long for that, none.
+void plan_ring(NormArgs* a, const NormShape& s, bool vec, bool x_f32, bool y_f32, int threads_per_sm, bool may_stage) {
+  uint32_t off = 0;
+  auto place = [&](RowSrc* r, bool f32) {
+    if (!r->p) return;
+    r->off = off;
+    off += vec ? static_cast<uint32_t>(s.T * s.vpt * 8 * (f32 ? 4 : 2))
+               : static_cast<uint32_t>(align_up(static_cast<size_t>(a->H) * (f32 ? 4 : 2), 16) + 16);
+  };
+  place(&a->dr, x_f32);
+  place(&a->x, x_f32);
+  place(&a->dn, a->n_f32);
+  place(&a->y, y_f32);
+  place(&a->gate, a->gate_f32);
+  a->stage_bytes = off;
+  const int ctas = std::min(16, std::max(1, threads_per_sm / s.T));
+  const uint32_t room = 216 * 1024 / ctas;
+  a->stages = may_stage ? static_cast<int>(std::min(4u, room / std::max(1u, off))) : 0;
+  if (a->stages < 2) a->stages = may_stage && 2 * off <= 216 * 1024 ? 2 : 0;
+}
+
+template <class K>
+cudaError_t launch_kernel(K kernel, const NormArgs& a, const NormShape& s, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
+  if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
+  kernel<<<s.grid, s.T, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool BWD, class XT, class YT, int VPT>
+cudaError_t launch_groups(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
+  if constexpr (BWD)
+    return vec ? launch_kernel(block_norm_backward_kernel<XT, YT, VPT, true>, a, s, stream)
+               : launch_kernel(block_norm_backward_kernel<XT, YT, VPT, false>, a, s, stream);
+  else
+    return vec ? launch_kernel(block_norm_forward_kernel<XT, YT, VPT, true>, a, s, stream)
+               : launch_kernel(block_norm_forward_kernel<XT, YT, VPT, false>, a, s, stream);
 }
 
 template <bool BWD, class XT, class YT>
-void launch_typed(const NormArgs& a, const NormShape& s, int grid, bool vec, cudaStream_t stream) {
-  const dim3 block(s.T, s.rows);
-  auto go = [&](auto vpt) {
-    constexpr int V = decltype(vpt)::value;
-    if constexpr (BWD) {
-      if (vec)
-        block_norm_backward_kernel<XT, YT, V, true><<<grid, block, 0, stream>>>(a);
-      else
-        block_norm_backward_kernel<XT, YT, V, false><<<grid, block, 0, stream>>>(a);
-    } else {
-      if (vec)
-        block_norm_forward_kernel<XT, YT, V, true><<<grid, block, 0, stream>>>(a);
-      else
-        block_norm_forward_kernel<XT, YT, V, false><<<grid, block, 0, stream>>>(a);
-    }
-  };
-  if (s.vpt == 1)
-    go(std::integral_constant<int, 1>());
-  else if (s.vpt == 2)
-    go(std::integral_constant<int, 2>());
-  else
-    go(std::integral_constant<int, 4>());
+cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
+  if (s.vpt == 1) return launch_groups<BWD, XT, YT, 1>(a, s, vec, stream);
+  if (s.vpt == 2) return launch_groups<BWD, XT, YT, 2>(a, s, vec, stream);
+  return launch_groups<BWD, XT, YT, 4>(a, s, vec, stream);
 }
 
 template <bool BWD>
-void launch(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, int grid, bool vec, cudaStream_t stream) {
+cudaError_t launch(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec, cudaStream_t stream) {
   if (x_f32)
-    y_f32 ? launch_typed<BWD, float, float>(a, s, grid, vec, stream)
-          : launch_typed<BWD, float, uint16_t>(a, s, grid, vec, stream);
-  else
-    y_f32 ? launch_typed<BWD, uint16_t, float>(a, s, grid, vec, stream)
-          : launch_typed<BWD, uint16_t, uint16_t>(a, s, grid, vec, stream);
+    return y_f32 ? launch_typed<BWD, float, float>(a, s, vec, stream) : launch_typed<BWD, float, uint16_t>(a, s, vec, stream);
+  return y_f32 ? launch_typed<BWD, uint16_t, float>(a, s, vec, stream)
+               : launch_typed<BWD, uint16_t, uint16_t>(a, s, vec, stream);
 }
 
 bool is_dtype(int d) { return d == E4B_F32 || d == E4B_BF16; }
 bool on_element(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == E4B_F32 ? 3u : 1u)) == 0;
 }
+
+// 8 elements of a base like this are one 16-byte (bf16) or 32-byte (fp32) vector.
+bool vec_base(const void* p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == E4B_F32 ? 31u : 15u)) == 0; }
 
 // What the two calls check alike.
 e4b_status check_norm(const e4b_block_norm* p, int64_t M, const void* y, const void* gate, e4b_gate_kind kind,
@@ -465,22 +627,28 @@ e4b_status check_norm(const e4b_block_norm* p, int64_t M, const void* y, const v
   return E4B_OK;
 }
 
-// One tensor of rows: its type, stride and alignment.  `vec` stays true while
-// 8 columns of every row can be moved as 16-byte vectors.
-e4b_status check_rows(const char* name, const void* p, int dtype, int64_t ld, int64_t H, bool* vec) {
+// How a call's rows can be moved: as vectors of 8 columns, or else in units of 16 bytes.
+struct Moves {
+  bool vec, units;
+};
+
+// One tensor of rows: its type, stride and alignment.
+e4b_status check_rows(const char* name, const void* p, int dtype, int64_t ld, int64_t H, Moves* moves) {
   if (!p) return E4B_OK;
   if (!is_dtype(dtype)) return fail(E4B_ERR_INVALID_ARGUMENT, std::string(name) + "'s type must be F32 or BF16");
   if (ld < H) return fail(E4B_ERR_INVALID_ARGUMENT, std::string(name) + "'s leading dimension must be >= H");
   if (!on_element(p, dtype)) return fail(E4B_ERR_INVALID_ARGUMENT, std::string(name) + " must be aligned to its elements");
-  *vec = *vec && aligned16(p) && ld % 8 == 0;
+  moves->vec = moves->vec && vec_base(p, dtype) && ld % 8 == 0;
+  moves->units = moves->units && aligned16(p);
   return E4B_OK;
 }
 
-NormArgs norm_args(const e4b_block_norm* p, int64_t M, const void* y, const void* gate, e4b_gate_kind kind,
+NormArgs norm_args(const e4b_block_norm* p, int64_t M, const void* y, int64_t ldy, const void* gate, e4b_gate_kind kind,
                    e4b_dtype gate_dtype, e4b_dtype n_dtype) {
   NormArgs a{};
-  a.y = y;
-  a.gate = gate;
+  a.y = {y, ldy, 0};
+  (kind == E4B_GATE_FULL ? a.gate.p : a.vec_gate) = gate;
+  a.gate.ld = p->H;
   a.w_post = p->w_post;
   a.w_next = p->w_next;
   a.M = M;
@@ -495,6 +663,17 @@ NormArgs norm_args(const e4b_block_norm* p, int64_t M, const void* y, const void
   a.eps = p->eps;
   a.inv_h = 1.0f / static_cast<float>(p->H);
   return a;
+}
+
+// Whether weights, gate and (backward) its gradient allow vectors and units.
+Moves moves_of(const e4b_block_norm* p, const void* gate, e4b_gate_kind kind, e4b_dtype gate_dtype, const void* dgate) {
+  Moves m{p->H % 8 == 0 && vec_base(p->w_post, p->w_dtype) && vec_base(p->w_next, p->w_dtype), true};
+  if (kind == E4B_GATE_CHANNEL || kind == E4B_GATE_FULL) m.vec = m.vec && vec_base(gate, gate_dtype);
+  if (kind == E4B_GATE_FULL) {
+    m.vec = m.vec && vec_base(dgate, gate_dtype);
+    m.units = aligned16(gate);
+  }
+  return m;
 }
 
 }  // namespace
@@ -514,42 +693,37 @@ e4b_status e4b_block_norm_forward(const void* x, e4b_dtype x_dtype, int64_t ldx,
   if (M > 0 && (y != nullptr) != (r != nullptr)) return fail(E4B_ERR_INVALID_ARGUMENT, "r is written exactly when y is given");
   if (M > 0 && (norm->w_next != nullptr) != (n != nullptr))
     return fail(E4B_ERR_INVALID_ARGUMENT, "n is written exactly when w_next is given");
-  bool vec = norm->H % 8 == 0 && aligned16(norm->w_post) && aligned16(norm->w_next) &&
-             (gate_kind < E4B_GATE_CHANNEL || gate_kind == E4B_GATE_TOKEN || aligned16(gate));
-  if (e4b_status s = check_rows("x", x, x_dtype, ldx, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("y", y, y_dtype, ldy, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("r", r, x_dtype, ldr, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("n", n, n_dtype, ldn, norm->H, &vec); s != E4B_OK) return s;
+  Moves moves = moves_of(norm, gate, gate_kind, gate_dtype, nullptr);
+  if (e4b_status s = check_rows("x", x, x_dtype, ldx, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("y", y, y_dtype, ldy, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("r", r, x_dtype, ldr, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("n", n, n_dtype, ldn, norm->H, &moves); s != E4B_OK) return s;
   if (e4b_status s = check_sm100(); s != E4B_OK) return s;
   if (M == 0) {
     set_path("block_norm.empty");
     return E4B_OK;
   }
-  NormArgs a = norm_args(norm, M, y, gate, gate_kind, gate_dtype, n_dtype);
-  a.x = x;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  NormArgs a = norm_args(norm, M, y, ldy, gate, gate_kind, gate_dtype, n_dtype);
+  a.x = {x, ldx, 0};
   a.r = r;
   a.n = n;
-  a.ldx = ldx;
-  a.ldy = ldy;
   a.ldr = ldr;
   a.ldn = ldn;
-  // A few rows leave most SMs idle: the widest split of a row is the shortest.
-  const NormShape s = norm_shape(a.H, M < 296 ? 1 : 4);
-  {
-    LaunchScope ls("block_norm.forward", reinterpret_cast<cudaStream_t>(stream));
-    launch<false>(a, x_dtype == E4B_F32, y && y_dtype == E4B_F32, s, static_cast<int>((M + s.rows - 1) / s.rows), vec,
-                  reinterpret_cast<cudaStream_t>(stream));
-  }
-  if (cudaError_t err = cudaGetLastError(); err != cudaSuccess) return cuda_fail(err, "block norm forward launch");
-  set_path(vec ? "block_norm.forward" : "block_norm.forward.scalar");
+  const NormShape s = norm_shape(M, a.H, kForwardThreads);
+  const bool x_f32 = x_dtype == E4B_F32, y_f32 = y && y_dtype == E4B_F32;
+  plan_ring(&a, s, moves.vec, x_f32, y_f32, kForwardThreads, moves.vec || moves.units);
+  LaunchScope ls("block_norm.forward", st);
+  if (cudaError_t err = launch<false>(a, x_f32, y_f32, s, moves.vec, st); err != cudaSuccess)
+    return cuda_fail(err, "block norm forward launch");
+  set_path(moves.vec ? "block_norm.forward" : "block_norm.forward.scalar");
   return E4B_OK;
 }
 
 size_t e4b_block_norm_backward_workspace_size(int64_t M, const e4b_block_norm* norm) {
   if (!norm || M < 1 || norm->H < 1 || norm->H > kMaxNormH) return 0;
-  int grid = 0;
-  const int parts = backward_parts(M, norm_shape(static_cast<int>(norm->H), 1), &grid);
-  return static_cast<size_t>(3) * parts * norm->H * sizeof(float);
+  const NormShape s = norm_shape(M, static_cast<int>(norm->H), kBackwardThreads);
+  return static_cast<size_t>(3) * s.grid * norm->H * sizeof(float);
 }
 
 e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn, e4b_dtype n_dtype, int64_t lddn,
@@ -567,15 +741,13 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
   if ((dy && !y && M > 0) || (dgate && gate_kind == E4B_GATE_NONE) || (dw_post && !norm->w_post) ||
       (dw_next && !norm->w_next))
     return fail(E4B_ERR_INVALID_ARGUMENT, "a gradient is asked for of an input that the block does not have");
-  bool vec = norm->H % 8 == 0 && aligned16(norm->w_post) && aligned16(norm->w_next) &&
-             (gate_kind == E4B_GATE_NONE || gate_kind == E4B_GATE_TOKEN || aligned16(gate)) &&
-             (gate_kind != E4B_GATE_FULL || aligned16(dgate));
-  if (e4b_status s = check_rows("dr", dr, x_dtype, lddr, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("dn", dn, n_dtype, lddn, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("r", r, x_dtype, ldr, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("y", y, y_dtype, ldy, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("dx", dx, x_dtype, lddx, norm->H, &vec); s != E4B_OK) return s;
-  if (e4b_status s = check_rows("dy", dy, y_dtype, lddy, norm->H, &vec); s != E4B_OK) return s;
+  Moves moves = moves_of(norm, gate, gate_kind, gate_dtype, dgate);
+  if (e4b_status s = check_rows("dr", dr, x_dtype, lddr, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("dn", dn, n_dtype, lddn, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("r", r, x_dtype, ldr, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("y", y, y_dtype, ldy, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("dx", dx, x_dtype, lddx, norm->H, &moves); s != E4B_OK) return s;
+  if (e4b_status s = check_rows("dy", dy, y_dtype, lddy, norm->H, &moves); s != E4B_OK) return s;
   if (!on_element(dgate, gate_kind == E4B_GATE_CHANNEL ? E4B_F32 : gate_dtype) || !on_element(dw_post, E4B_F32) ||
       !on_element(dw_next, E4B_F32))
     return fail(E4B_ERR_INVALID_ARGUMENT, "dgate, dw_post and dw_next must be aligned to their elements");
@@ -585,29 +757,27 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
     return s;
   if (e4b_status s = check_sm100(); s != E4B_OK) return s;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  NormArgs a = norm_args(norm, M, y, gate, gate_kind, gate_dtype, n_dtype);
-  a.dr = dr;
-  a.dn = dn;
-  a.x = nullptr;
-  a.r = const_cast<void*>(r);
+  NormArgs a = norm_args(norm, M, y, ldy, gate, gate_kind, gate_dtype, n_dtype);
+  a.dr = {dr, lddr, 0};
+  a.dn = {dn, lddn, 0};
+  if (norm->w_next) a.x = {r, ldr, 0};
   a.dx = dx;
   a.dy = dy;
   a.dgate = dgate;
   a.partial = static_cast<float*>(workspace);
-  a.lddr = lddr;
-  a.ldn = lddn;
-  a.ldr = ldr;
-  a.ldy = ldy;
   a.lddx = lddx;
   a.lddy = lddy;
   if (M > 0) {
-    const NormShape s = norm_shape(a.H, 1);
-    int grid = 0;
-    a.parts = backward_parts(M, s, &grid);
+    const NormShape s = norm_shape(M, a.H, kBackwardThreads);
+    a.parts = s.grid;
+    const bool x_f32 = x_dtype == E4B_F32, y_f32 = y && y_dtype == E4B_F32;
+    // the partial sums' rows are vectors of 32 bytes
+    const bool vec = moves.vec && vec_base(workspace, E4B_F32);
+    plan_ring(&a, s, vec, x_f32, y_f32, kBackwardThreads, vec || moves.units);
     LaunchScope ls("block_norm.backward", st);
-    launch<true>(a, x_dtype == E4B_F32, y && y_dtype == E4B_F32, s, grid, vec, st);
+    if (cudaError_t err = launch<true>(a, x_f32, y_f32, s, vec, st); err != cudaSuccess)
+      return cuda_fail(err, "block norm backward launch");
   }
-  if (cudaError_t err = cudaGetLastError(); err != cudaSuccess) return cuda_fail(err, "block norm backward launch");
   float* dchannel = gate_kind == E4B_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
   if (dw_post || dw_next || dchannel) {
     ReduceArgs ra{a.partial, {dw_post, dw_next, dchannel}, a.parts, a.H};
@@ -615,7 +785,7 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
     block_norm_reduce_kernel<<<dim3((a.H + kRedCols - 1) / kRedCols, 3), dim3(kRedCols, kRedLanes), 0, st>>>(ra);
   }
   if (cudaError_t err = cudaGetLastError(); err != cudaSuccess) return cuda_fail(err, "block norm reduce launch");
-  set_path(M == 0 ? "block_norm.backward.empty" : vec ? "block_norm.backward" : "block_norm.backward.scalar");
+  set_path(M == 0 ? "block_norm.backward.empty" : moves.vec ? "block_norm.backward" : "block_norm.backward.scalar");
   return E4B_OK;
 }
 
