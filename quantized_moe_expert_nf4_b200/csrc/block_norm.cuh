@@ -1,0 +1,357 @@
+// Kernels of the block norms (included by the forward's and the backward's
+// translation units).
+#pragma once
+
+#include "common.cuh"
+#include "e4b_internal.h"
+
+namespace e4b {
+
+constexpr int kMaxNormThreads = 512;
+
+// A tensor of rows that a kernel reads: leading dimension in elements, place in a
+// ring stage.
+struct RowSrc {
+  const void* p;
+  int64_t ld;
+  uint32_t off;
+};
+
+struct NormArgs {
+  RowSrc x, y, gate;                 // x: also r of the backward; gate: E4B_GATE_FULL's rows
+  RowSrc dr, dn;                     // backward
+  const void *vec_gate, *w_post, *w_next;  // vec_gate: channel or token gate
+  void *r, *n;                       // forward
+  void *dx, *dy, *dgate;             // backward
+  float* partial;                    // backward: [3][parts][H] column sums (w_post, w_next, channel gate)
+  int64_t ldr, ldn, lddx, lddy;      // of the outputs
+  int64_t M;
+  int H, parts;
+  int stages;                        // of the ring; 0: rows are read from memory directly
+  uint32_t stage_bytes;
+  int gate_kind, gate_f32, sigmoid, w_f32, n_f32;
+  float scale, offset, eps, inv_h;
+};
+
+// Threads of a CTA and the groups of 8 columns that each takes.
+struct NormShape {
+  int T, vpt, grid;
+};
+// Most threads of a CTA, and CTAs an SM should hold, by the groups of a thread.
+constexpr int norm_threads(int vpt) { return vpt == 4 ? 512 : 384; }
+
+// Launchers; vec: all rows can be moved as vectors of 8 columns (the ring is used).
+cudaError_t launch_block_norm_forward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec,
+                                      cudaStream_t stream);
+cudaError_t launch_block_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec,
+                                       cudaStream_t stream);
+
+// ---- pairs of floats --------------------------------------------------------------
+// Elementwise work on two columns per instruction (the packed fp32 forms of sm_100).
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float lo(F2 a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+  return x;
+}
+__device__ __forceinline__ float hi(F2 a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+  return y;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// Eight columns.
+struct F8 {
+  F2 p[4];
+};
+__device__ __forceinline__ F8 zero8() { return {{f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)}}; }
+__device__ __forceinline__ F8 fill8(float x) { return {{f2(x), f2(x), f2(x), f2(x)}}; }
+__device__ __forceinline__ F8 operator*(const F8& a, const F8& b) {
+  return {{a.p[0] * b.p[0], a.p[1] * b.p[1], a.p[2] * b.p[2], a.p[3] * b.p[3]}};
+}
+__device__ __forceinline__ F8 operator*(const F8& a, F2 b) { return {{a.p[0] * b, a.p[1] * b, a.p[2] * b, a.p[3] * b}}; }
+__device__ __forceinline__ F8 operator+(const F8& a, F2 b) { return {{a.p[0] + b, a.p[1] + b, a.p[2] + b, a.p[3] + b}}; }
+__device__ __forceinline__ F8 fma8(const F8& a, const F8& b, const F8& c) {
+  return {{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1]), fma2(a.p[2], b.p[2], c.p[2]), fma2(a.p[3], b.p[3], c.p[3])}};
+}
+__device__ __forceinline__ F8 fma8(const F8& a, F2 b, const F8& c) {
+  return {{fma2(a.p[0], b, c.p[0]), fma2(a.p[1], b, c.p[1]), fma2(a.p[2], b, c.p[2]), fma2(a.p[3], b, c.p[3])}};
+}
+// s + a . b, column pairs apart
+__device__ __forceinline__ F2 dot8(const F8& a, const F8& b, F2 s) {
+  return fma2(a.p[3], b.p[3], fma2(a.p[2], b.p[2], fma2(a.p[1], b.p[1], fma2(a.p[0], b.p[0], s))));
+}
+__device__ __forceinline__ float get8(const F8& a, int j) { return j & 1 ? hi(a.p[j >> 1]) : lo(a.p[j >> 1]); }
+__device__ __forceinline__ F8 set8(const float v[8]) { return {{f2(v[0], v[1]), f2(v[2], v[3]), f2(v[4], v[5]), f2(v[6], v[7])}}; }
+
+// ---- memory ---------------------------------------------------------------------------
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_bits_to_float(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = float_to_bf16_bits(v); }
+
+__device__ __forceinline__ F8 unpack8(uint4 q) {
+  return {{f2(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u)),
+           f2(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u)),
+           f2(__uint_as_float(q.z << 16), __uint_as_float(q.z & 0xffff0000u)),
+           f2(__uint_as_float(q.w << 16), __uint_as_float(q.w & 0xffff0000u))}};
+}
+__device__ __forceinline__ F8 join8(float4 a, float4 b) { return {{f2(a.x, a.y), f2(a.z, a.w), f2(b.x, b.y), f2(b.z, b.w)}}; }
+__device__ __forceinline__ F8 load8(const float* p) {
+  return join8(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4));
+}
+__device__ __forceinline__ F8 load8(const uint16_t* p) { return unpack8(*reinterpret_cast<const uint4*>(p)); }
+// One 32-byte store: two of 16 bytes would each write half of every sector.
+__device__ __forceinline__ void store8(float* p, const F8& v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(lo(v.p[0])), "f"(hi(v.p[0])),
+               "f"(lo(v.p[1])), "f"(hi(v.p[1])), "f"(lo(v.p[2])), "f"(hi(v.p[2])), "f"(lo(v.p[3])), "f"(hi(v.p[3]))
+               : "memory");
+}
+__device__ __forceinline__ void store8(uint16_t* p, const F8& v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(lo(v.p[0]), hi(v.p[0])), pack_bf16x2(lo(v.p[1]), hi(v.p[1])),
+                                            pack_bf16x2(lo(v.p[2]), hi(v.p[2])), pack_bf16x2(lo(v.p[3]), hi(v.p[3])));
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16(void* dst, const void* src, int bytes) {  // the rest of the unit becomes zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+// Through L1: the two halves of a 32-byte sector are asked for by two instructions.
+__device__ __forceinline__ void cp16_l1(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the newest stages - 2 groups are in (stages is 2 to 4).
+__device__ __forceinline__ void cp_wait(int stages) {
+  if (stages == 4)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (stages == 3)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// One thread's share of a row: VPT groups of 8 columns.  VEC: a group is 8
+// adjacent columns, moved as vectors; otherwise its columns lie T apart, so
+// that a warp's accesses stay adjacent.
+template <int VPT, bool VEC>
+struct Cols {
+  int T, t, H;
+  __device__ __forceinline__ int col(int v, int j) const { return VEC ? (v * T + t) * 8 + j : (v * 8 + j) * T + t; }
+  __device__ __forceinline__ bool in(int v) const { return (v * T + t) * 8 < H; }  // VEC
+  // Columns past H read as zero and are not written.
+  template <class E>
+  __device__ __forceinline__ F8 load(const E* row, int v) const {
+    if constexpr (VEC) {
+      return in(v) ? load8(row + col(v, 0)) : zero8();
+    } else {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = col(v, j) < H ? load1(row + col(v, j)) : 0.0f;
+      return set8(f);
+    }
+  }
+  template <class E>
+  __device__ __forceinline__ void store(E* row, int v, const F8& f) const {
+    if constexpr (VEC) {
+      if (in(v)) store8(row + col(v, 0), f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col(v, j) < H) store1(row + col(v, j), get8(f, j));
+    }
+  }
+  // The element type known at run time only (uniform over the launch).
+  __device__ __forceinline__ F8 load(const void* row, int f32, int v) const {
+    return f32 ? load(static_cast<const float*>(row), v) : load(static_cast<const uint16_t*>(row), v);
+  }
+  __device__ __forceinline__ void store(void* base, int64_t off, int f32, int v, const F8& f) const {
+    if (f32)
+      store(static_cast<float*>(base) + off, v, f);
+    else
+      store(static_cast<uint16_t*>(base) + off, v, f);
+  }
+
+  // Row m of `s` into its place in `stage`.
+  template <class E>
+  __device__ __forceinline__ void fetch(unsigned char* stage, const RowSrc& s, int64_t m, int64_t M) const {
+    const E* row = static_cast<const E*>(s.p) + m * s.ld;
+    unsigned char* dst = stage + s.off;
+    if constexpr (VEC) {
+      // 8 bf16: one unit per thread; 8 floats: two, in two planes
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        if (!in(v)) continue;
+        if constexpr (sizeof(E) == 2) {
+          cp16(dst + (v * T + t) * 16, row + col(v, 0));
+        } else {
+          cp16_l1(dst + (v * T + t) * 16, row + col(v, 0));
+          cp16_l1(dst + ((VPT + v) * T + t) * 16, row + col(v, 0) + 4);
+        }
+      }
+    } else {
+      // the 16-byte units that the row touches: its neighbours' ends come along,
+      // but nothing past the last row's end
+      const uintptr_t at = reinterpret_cast<uintptr_t>(row), lead = at & 15;
+      const uintptr_t end = at + ((M - 1 - m) * s.ld + H) * sizeof(E);
+      const int bytes = static_cast<int>(lead) + H * static_cast<int>(sizeof(E));
+      for (int u = t; u * 16 < bytes; u += T) {
+        const uintptr_t from = at - lead + u * 16;
+        cp16(dst + u * 16, reinterpret_cast<const void*>(from), end - from < 16 ? static_cast<int>(end - from) : 16);
+      }
+    }
+  }
+  // VEC: the places of columns past H in a stage, which fetch() leaves alone.
+  template <class E>
+  __device__ __forceinline__ void clear(unsigned char* stage, const RowSrc& s) const {
+    if (!s.p) return;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      if (!in(v))
+        for (int plane = 0; plane < static_cast<int>(sizeof(E)) / 2; ++plane)
+          *reinterpret_cast<uint4*>(stage + s.off + ((plane * VPT + v) * T + t) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  // Group v of row m, from the stage that fetch() filled.
+  template <class E>
+  __device__ __forceinline__ F8 staged(const unsigned char* stage, const RowSrc& s, int64_t m, int v) const {
+    const unsigned char* src = stage + s.off;
+    if constexpr (VEC) {
+      const uint4 q = *reinterpret_cast<const uint4*>(src + (v * T + t) * 16);
+      if constexpr (sizeof(E) == 2) return unpack8(q);
+      const uint4 u = *reinterpret_cast<const uint4*>(src + ((VPT + v) * T + t) * 16);
+      return {{f2(__uint_as_float(q.x), __uint_as_float(q.y)), f2(__uint_as_float(q.z), __uint_as_float(q.w)),
+               f2(__uint_as_float(u.x), __uint_as_float(u.y)), f2(__uint_as_float(u.z), __uint_as_float(u.w))}};
+    } else {
+      const uintptr_t lead = reinterpret_cast<uintptr_t>(static_cast<const E*>(s.p) + m * s.ld) & 15;
+      return load(reinterpret_cast<const E*>(src + lead), v);
+    }
+  }
+};
+
+__device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ F8 sigmoid8(const F8& g) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = sigmoid_f32(get8(g, j));
+  return set8(f);
+}
+
+// The rows of a CTA, one after another.  VEC always has a ring; other rows have
+// one unless they are too long for it or their bases are not 16-byte aligned.
+template <class XT, class YT, int VPT, bool VEC, bool BWD>
+struct Rows {
+  const NormArgs& a;
+  const Cols<VPT, VEC>& c;
+  unsigned char* ring;
+  unsigned char* cur;
+  int put_stage = 0, stage = 0;
+  int64_t put_row;
+
+  __device__ __forceinline__ bool ringed() const { return VEC || a.stages; }
+  __device__ __forceinline__ Rows(const NormArgs& a_, const Cols<VPT, VEC>& c_, unsigned char* ring_)
+      : a(a_), c(c_), ring(ring_), cur(ring_), put_row(blockIdx.x) {
+    if constexpr (VEC) {
+      for (int i = 0; i < a.stages; ++i) {
+        unsigned char* to = ring + i * a.stage_bytes;
+        c.template clear<XT>(to, a.dr);
+        c.template clear<XT>(to, a.x);
+        a.n_f32 ? c.template clear<float>(to, a.dn) : c.template clear<uint16_t>(to, a.dn);
+        c.template clear<YT>(to, a.y);
+        a.gate_f32 ? c.template clear<float>(to, a.gate) : c.template clear<uint16_t>(to, a.gate);
+      }
+    }
+    for (int i = 0; i + 1 < a.stages; ++i) put();
+  }
+  __device__ __forceinline__ void put() {
+    if (put_row < a.M) {
+      unsigned char* to = ring + put_stage * a.stage_bytes;
+      if (!BWD || a.w_next) c.template fetch<XT>(to, a.x, put_row, a.M);
+      if (a.y.p) c.template fetch<YT>(to, a.y, put_row, a.M);
+      if constexpr (BWD) {
+        if (a.dr.p) c.template fetch<XT>(to, a.dr, put_row, a.M);
+        if (a.w_next) a.n_f32 ? c.template fetch<float>(to, a.dn, put_row, a.M) : c.template fetch<uint16_t>(to, a.dn, put_row, a.M);
+      }
+      if (a.gate.p) a.gate_f32 ? c.template fetch<float>(to, a.gate, put_row, a.M) : c.template fetch<uint16_t>(to, a.gate, put_row, a.M);
+      put_row += gridDim.x;
+    }
+    cp_commit();
+    put_stage = put_stage + 1 == a.stages ? 0 : put_stage + 1;
+  }
+  // Makes the next row readable and sets off the row `stages - 1` further on.  The
+  // stage that it fills is the last row's: this thread's own part of it, or,
+  // read across threads, behind a barrier that they all reach after it.
+  __device__ __forceinline__ void next() {
+    if (!ringed()) return;
+    cp_wait(a.stages);
+    if constexpr (!VEC) __syncthreads();
+    put();
+    cur = ring + stage * a.stage_bytes;
+    stage = stage + 1 == a.stages ? 0 : stage + 1;
+  }
+  template <class E>
+  __device__ __forceinline__ F8 load(const RowSrc& s, int64_t m, int v) const {
+    if (ringed()) return c.template staged<E>(cur, s, m, v);
+    return c.load(static_cast<const E*>(s.p) + m * s.ld, v);
+  }
+  __device__ __forceinline__ F8 load(const RowSrc& s, int64_t m, int f32, int v) const {
+    return f32 ? load<float>(s, m, v) : load<uint16_t>(s, m, v);
+  }
+  // The gate of a group of columns (before any sigmoid).
+  __device__ __forceinline__ F8 gate(int64_t m, int v) const {
+    if (a.gate_kind == E4B_GATE_FULL) return load(a.gate, m, a.gate_f32, v);
+    if (a.gate_kind == E4B_GATE_CHANNEL) return c.load(a.vec_gate, a.gate_f32, v);
+    return fill8(a.gate_f32 ? load1(static_cast<const float*>(a.vec_gate) + m)
+                            : load1(static_cast<const uint16_t*>(a.vec_gate) + m));
+  }
+};
+
+// Sums of up to three values over the CTA's T threads (a multiple of 32, at most
+// 512).  One barrier above one warp: a caller that sums again passes another buffer.
+template <int NV>
+__device__ __forceinline__ void row_sum(float v[NV], int T, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (T == 32) return;
+  const int lane = threadIdx.x & 31, warps = T >> 5;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) red[i * 16 + (threadIdx.x >> 5)] = v[i];
+  __syncthreads();
+  // every warp adds the warps' sums alike: lanes w and w + 16 hold warp w's
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = (lane & 15) < warps ? red[i * 16 + (lane & 15)] : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+
+}  // namespace e4b

@@ -1,0 +1,132 @@
+// Backward of the block norms: see block_norm.cu for the formulas.
+#include "block_norm.cuh"
+
+namespace e4b {
+namespace {
+
+template <class XT, class YT, int VPT, bool VEC>
+__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1) block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  // Buffers alternate by row: a row may have one sum only, and so no other
+  // barrier before the next row's.
+  __shared__ float red[2][2][3 * 16];
+  const int T = blockDim.x;
+  const Cols<VPT, VEC> c{T, static_cast<int>(threadIdx.x), a.H};
+  Rows<XT, YT, VPT, VEC, true> rows(a, c, ring);
+  const bool has_y = a.y.p != nullptr, next = a.w_next != nullptr, post = a.w_post != nullptr;
+  const int kind = a.gate_kind;
+  const F2 offset = f2(a.offset);
+  F8 s_post[VPT], s_next[VPT], s_gate[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) s_post[v] = s_next[v] = s_gate[v] = zero8();
+  int odd = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, odd ^= 1) {
+    rows.next();
+    F2 t0 = f2(0.0f), t1 = t0, t2 = t0;  // r^2, h * r, y^2
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (has_y) {
+        const F8 y = rows.template load<YT>(a.y, m, v);
+        t2 = dot8(y, y, t2);
+      }
+      if (next) {
+        const F8 r = rows.template load<XT>(a.x, m, v);
+        const F8 h = rows.load(a.dn, m, a.n_f32, v) * (c.load(a.w_next, a.w_f32, v) + offset);
+        t0 = dot8(r, r, t0);
+        t1 = dot8(h, r, t1);
+      }
+    }
+    float s1[3] = {lo(t0) + hi(t0), lo(t1) + hi(t1), lo(t2) + hi(t2)};
+    row_sum<3>(s1, T, red[odd][0]);
+    const float rstd_r = rsqrtf(s1[0] * a.inv_h + a.eps), rstd_y = post ? rsqrtf(s1[2] * a.inv_h + a.eps) : 1.0f;
+    const float mean_r = s1[1] * rstd_r * a.inv_h;  // mean(h * rhat)
+    F8 k[VPT];
+    F2 u0 = f2(0.0f), u1 = u0;  // k * yhat, d * z * slope
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      F8 d = a.dr.p ? rows.template load<XT>(a.dr, m, v) : zero8();
+      if (next) {
+        const F8 hat = rows.template load<XT>(a.x, m, v) * f2(rstd_r);
+        const F8 dn = rows.load(a.dn, m, a.n_f32, v);
+        const F8 h = dn * (c.load(a.w_next, a.w_f32, v) + offset);
+        s_next[v] = fma8(dn, hat, s_next[v]);
+        d = fma8(fma8(hat, f2(-mean_r), h), f2(rstd_r), d);
+      }
+      if (a.dx) c.store(static_cast<XT*>(a.dx) + m * a.lddx, v, d);
+      if (!has_y) continue;
+      const F8 hat = rows.template load<YT>(a.y, m, v) * f2(rstd_y);
+      const F8 w = post ? c.load(a.w_post, a.w_f32, v) + offset : fill8(1.0f);
+      F8 dz = d * f2(a.scale);
+      if (kind != E4B_GATE_NONE) {
+        F8 f = rows.gate(m, v);
+        F8 dg = dz * (hat * w);
+        if (a.sigmoid) {
+          f = sigmoid8(f);
+          dg = dg * (f * (fma8(f, f2(-1.0f), fill8(1.0f))));
+        }
+        dz = dz * f;
+        if (kind == E4B_GATE_CHANNEL)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s_gate[v].p[j] = s_gate[v].p[j] + dg.p[j];
+        else if (kind == E4B_GATE_TOKEN)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u1 = u1 + dg.p[j];
+        else if (a.dgate)
+          c.store(a.dgate, m * a.H, a.gate_f32, v, dg);
+      }
+      s_post[v] = fma8(dz, hat, s_post[v]);
+      k[v] = dz * w;
+      u0 = dot8(k[v], hat, u0);
+    }
+    if (!has_y) continue;
+    float s2[2] = {lo(u0) + hi(u0), lo(u1) + hi(u1)};
+    if (post || kind == E4B_GATE_TOKEN) row_sum<2>(s2, T, red[odd][1]);
+    if (kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0) {
+      if (a.gate_f32)
+        store1(static_cast<float*>(a.dgate) + m, s2[1]);
+      else
+        store1(static_cast<uint16_t*>(a.dgate) + m, s2[1]);
+    }
+    if (!a.dy) continue;
+    const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const F8 y = rows.template load<YT>(a.y, m, v);
+      c.store(static_cast<YT*>(a.dy) + m * a.lddy, v, fma8(y, f2(-mean_y), k[v]) * f2(rstd_y));
+    }
+  }
+  const int64_t plane = static_cast<int64_t>(a.parts) * a.H;
+  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.H;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (post) c.store(part, v, s_post[v]);
+    if (next) c.store(part + plane, v, s_next[v]);
+    if (kind == E4B_GATE_CHANNEL) c.store(part + 2 * plane, v, s_gate[v]);
+  }
+}
+
+template <class XT, class YT, int VPT>
+cudaError_t launch_groups(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
+  auto* kernel = vec ? block_norm_backward_kernel<XT, YT, VPT, true> : block_norm_backward_kernel<XT, YT, VPT, false>;
+  const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
+  if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
+  kernel<<<s.grid, s.T, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <class XT, class YT>
+cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
+  if (s.vpt == 1) return launch_groups<XT, YT, 1>(a, s, vec, stream);
+  if (s.vpt == 2) return launch_groups<XT, YT, 2>(a, s, vec, stream);
+  return launch_groups<XT, YT, 4>(a, s, vec, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec,
+                                       cudaStream_t stream) {
+  if (x_f32) return y_f32 ? launch_typed<float, float>(a, s, vec, stream) : launch_typed<float, uint16_t>(a, s, vec, stream);
+  return y_f32 ? launch_typed<uint16_t, float>(a, s, vec, stream) : launch_typed<uint16_t, uint16_t>(a, s, vec, stream);
+}
+
+}  // namespace e4b
