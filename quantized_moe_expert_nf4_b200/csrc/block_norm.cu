@@ -34,7 +34,8 @@ namespace {
 
 constexpr int kMaxNormH = 16384;
 
-template <class XT, class YT, int VPT, bool VEC>
+// Rows of any width, stride and base.
+template <class XT, class YT, int VPT>
 __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2 : 1)
     block_norm_forward_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
@@ -42,8 +43,8 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
   // barrier before the next row's.
   __shared__ float red[2][2][16];
   const int T = blockDim.x;
-  const Cols<VPT, VEC> c{T, static_cast<int>(threadIdx.x), a.H};
-  Rows<XT, YT, VPT, VEC, false> rows(a, c, ring);
+  const Cols<VPT> c{T, static_cast<int>(threadIdx.x), a.H};
+  Rows<XT, YT, VPT, false> rows(a, c, ring);
   const F2 offset = f2(a.offset);
   int odd = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, odd ^= 1) {
@@ -94,9 +95,116 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
   }
 }
 
+// Rows moved as vectors.  ALL: y and both weights are there, the step between two
+// blocks.
+template <class XT, class YT, int VPT, bool ALL>
+__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2 : 1)
+    block_norm_forward_vec_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float red[2][2][16];  // as above
+  const int T = blockDim.x;
+  const VecCols<VPT> c(T, threadIdx.x, a.H);
+  const bool has_y = ALL || a.y.p, next = ALL || a.w_next, post = ALL || a.w_post;
+  const int kind = a.gate_kind, stages = a.stages;
+  const int64_t step = gridDim.x;
+  const XT* x_p = static_cast<const XT*>(a.x.p) + blockIdx.x * a.x.ld;
+  const YT* y_p = static_cast<const YT*>(a.y.p) + blockIdx.x * a.y.ld;
+  const unsigned char* g_p = static_cast<const unsigned char*>(a.gate.p) + blockIdx.x * a.gate.ld * (a.gate_f32 ? 4 : 2);
+  const uint32_t ring_u = smem_addr(ring) + threadIdx.x * 16;
+  const unsigned char* ring_p = ring + threadIdx.x * 16;
+  int64_t put_row = blockIdx.x;
+  int put_stage = 0, stage = 0;
+  // A thread reads its own places only, so that filling the last row's stage needs no barrier.
+  auto put = [&]() {
+    if (put_row < a.M) {
+      const uint32_t to = ring_u + put_stage * a.stage_bytes;
+      c.fetch(to + a.x.off, x_p);
+      x_p += step * a.x.ld;
+      if (has_y) {
+        c.fetch(to + a.y.off, y_p);
+        y_p += step * a.y.ld;
+      }
+      if (kind == E4B_GATE_FULL) {
+        if (a.gate_f32)
+          c.fetch(to + a.gate.off, reinterpret_cast<const float*>(g_p));
+        else
+          c.fetch(to + a.gate.off, reinterpret_cast<const uint16_t*>(g_p));
+        g_p += step * a.gate.ld * (a.gate_f32 ? 4 : 2);
+      }
+      put_row += step;
+    }
+    cp_commit();
+    put_stage = put_stage + 1 == stages ? 0 : put_stage + 1;
+  };
+  for (int i = 0; i + 1 < stages; ++i) put();
+  const F2 offset = f2(a.offset);
+  XT* r_p = static_cast<XT*>(a.r) + blockIdx.x * a.ldr;
+  unsigned char* n_p = static_cast<unsigned char*>(a.n) + blockIdx.x * a.ldn * (a.n_f32 ? 4 : 2);
+  int odd = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, r_p += step * a.ldr, n_p += step * a.ldn * (a.n_f32 ? 4 : 2)) {
+    cp_wait(stages);
+    put();
+    const unsigned char* cur = ring_p + stage * a.stage_bytes;
+    stage = stage + 1 == stages ? 0 : stage + 1;
+    F8 r[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) r[v] = c.template staged<XT>(cur + a.x.off, v);
+    if (has_y) {
+      float factor = a.scale;  // residual scale and the row's 1 / rms
+      if (post) {
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const F8 y = c.template staged<YT>(cur + a.y.off, v);
+          const F2 q = dot8(y, y, f2(0.0f));
+          ss[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+        }
+        row_sum<1>(ss, T, red[odd][0]);
+        factor *= rsqrtf(ss[0] * a.inv_h + a.eps);
+      }
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        F8 z = c.template staged<YT>(cur + a.y.off, v) * f2(factor);
+        if (post) z = z * (c.vector(a.w_post, a.w_f32, v) + offset);
+        if (kind != E4B_GATE_NONE) {
+          F8 f = kind == E4B_GATE_CHANNEL ? c.vector(a.vec_gate, a.gate_f32, v)
+                 : kind == E4B_GATE_TOKEN ? fill8(load1(a.vec_gate, m, a.gate_f32))
+                 : a.gate_f32             ? c.template staged<float>(cur + a.gate.off, v)
+                                          : c.template staged<uint16_t>(cur + a.gate.off, v);
+          if (a.sigmoid) f = sigmoid8(f);
+          r[v] = fma8(z, f, r[v]);
+        } else {
+          r[v] = fma8(z, f2(1.0f), r[v]);
+        }
+        c.store(r_p, v, r[v]);
+      }
+    }
+    if (!next) continue;
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const F2 q = dot8(r[v], r[v], f2(0.0f));
+      ss[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+    }
+    row_sum<1>(ss, T, red[odd][1]);
+    const F2 rstd = f2(rsqrtf(ss[0] * a.inv_h + a.eps));
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const F8 n = r[v] * rstd * (c.vector(a.w_next, a.w_f32, v) + offset);
+      if (a.n_f32)
+        c.store(reinterpret_cast<float*>(n_p), v, n);
+      else
+        c.store(reinterpret_cast<uint16_t*>(n_p), v, n);
+    }
+  }
+}
+
 template <class XT, class YT, int VPT>
 cudaError_t launch_groups(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  auto* kernel = vec ? block_norm_forward_kernel<XT, YT, VPT, true> : block_norm_forward_kernel<XT, YT, VPT, false>;
+  const bool all = a.y.p && a.w_next && a.w_post;
+  auto* kernel = !vec  ? block_norm_forward_kernel<XT, YT, VPT>
+                 : all ? block_norm_forward_vec_kernel<XT, YT, VPT, true>
+                       : block_norm_forward_vec_kernel<XT, YT, VPT, false>;
   const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
   kernel<<<s.grid, s.T, smem, stream>>>(a);

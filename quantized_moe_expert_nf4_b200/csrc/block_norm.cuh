@@ -136,15 +136,15 @@ __device__ __forceinline__ void store8(uint16_t* p, const F8& v) {
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void cp16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp16(void* dst, const void* src, int bytes) {  // the rest of the unit becomes zero
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // the rest of the unit becomes zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Through L1: the two halves of a 32-byte sector are asked for by two instructions.
-__device__ __forceinline__ void cp16_l1(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp16_l1(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until all but the newest stages - 2 groups are in (stages is 2 to 4).
@@ -157,35 +157,93 @@ __device__ __forceinline__ void cp_wait(int stages) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// One thread's share of a row: VPT groups of 8 columns.  VEC: a group is 8
-// adjacent columns, moved as vectors; otherwise its columns lie T apart, so
-// that a warp's accesses stay adjacent.
-template <int VPT, bool VEC>
-struct Cols {
-  int T, t, H;
-  __device__ __forceinline__ int col(int v, int j) const { return VEC ? (v * T + t) * 8 + j : (v * 8 + j) * T + t; }
-  __device__ __forceinline__ bool in(int v) const { return (v * T + t) * 8 < H; }  // VEC
-  // Columns past H read as zero and are not written.
-  template <class E>
-  __device__ __forceinline__ F8 load(const E* row, int v) const {
-    if constexpr (VEC) {
-      return in(v) ? load8(row + col(v, 0)) : zero8();
-    } else {
-      float f[8];
+__device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ F8 sigmoid8(const F8& g) {
+  float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = col(v, j) < H ? load1(row + col(v, j)) : 0.0f;
-      return set8(f);
+  for (int j = 0; j < 8; ++j) f[j] = sigmoid_f32(get8(g, j));
+  return set8(f);
+}
+__device__ __forceinline__ float load1(const void* p, int64_t i, int f32) {
+  return f32 ? load1(static_cast<const float*>(p) + i) : load1(static_cast<const uint16_t*>(p) + i);
+}
+__device__ __forceinline__ void store1(void* p, int64_t i, int f32, float v) {
+  if (f32)
+    store1(static_cast<float*>(p) + i, v);
+  else
+    store1(static_cast<uint16_t*>(p) + i, v);
+}
+
+// ---- rows moved as vectors --------------------------------------------------------------
+// A thread's share of a row: VPT groups of 8 adjacent columns, group v of thread
+// t at column 8 (v T + t).  Groups past the row's end stand at column 0: they read
+// what is there, are left out of sums over columns, and are not written.
+template <int VPT>
+struct VecCols {
+  int T16;       // bytes of one plane of T 16-byte units
+  int col[VPT];  // first column of each group
+  bool in[VPT];
+  __device__ __forceinline__ VecCols(int T, int t, int H) : T16(T * 16) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int at = (v * T + t) * 8;
+      in[v] = at < H;
+      col[v] = in[v] ? at : 0;
+    }
+  }
+  // Into this thread's places of a ring stage (`dst`: its unit of plane 0) from a
+  // row: 8 bf16 are one unit, 8 floats two, in two planes.
+  template <class E>
+  __device__ __forceinline__ void fetch(uint32_t dst, const E* row) const {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const E* src = row + col[v];
+      if constexpr (sizeof(E) == 2) {
+        cp16(dst + v * T16, src);
+      } else {
+        cp16_l1(dst + v * T16, src);
+        cp16_l1(dst + (VPT + v) * T16, src + 4);
+      }
     }
   }
   template <class E>
+  __device__ __forceinline__ F8 staged(const unsigned char* src, int v) const {
+    const uint4 q = *reinterpret_cast<const uint4*>(src + v * T16);
+    if constexpr (sizeof(E) == 2) return unpack8(q);
+    const uint4 u = *reinterpret_cast<const uint4*>(src + (VPT + v) * T16);
+    return {{f2(__uint_as_float(q.x), __uint_as_float(q.y)), f2(__uint_as_float(q.z), __uint_as_float(q.w)),
+             f2(__uint_as_float(u.x), __uint_as_float(u.y)), f2(__uint_as_float(u.z), __uint_as_float(u.w))}};
+  }
+  // A vector over the columns (a weight, a channel gate): held in L1.
+  __device__ __forceinline__ F8 vector(const void* p, int f32, int v) const {
+    return f32 ? load8(static_cast<const float*>(p) + col[v]) : load8(static_cast<const uint16_t*>(p) + col[v]);
+  }
+  template <class E>
   __device__ __forceinline__ void store(E* row, int v, const F8& f) const {
-    if constexpr (VEC) {
-      if (in(v)) store8(row + col(v, 0), f);
-    } else {
+    if (in[v]) store8(row + col[v], f);
+  }
+};
+
+// ---- other rows -----------------------------------------------------------------------------
+// Columns j T + t, j < 8 VPT, of thread t, so that a warp's accesses are adjacent; a
+// group v is its columns j = 8 v .. 8 v + 7.  Columns past H read as zero and
+// are not written.
+template <int VPT>
+struct Cols {
+  int T, t, H;
+  __device__ __forceinline__ int col(int v, int j) const { return (v * 8 + j) * T + t; }
+  template <class E>
+  __device__ __forceinline__ F8 load(const E* row, int v) const {
+    float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col(v, j) < H) store1(row + col(v, j), get8(f, j));
-    }
+    for (int j = 0; j < 8; ++j) f[j] = col(v, j) < H ? load1(row + col(v, j)) : 0.0f;
+    return set8(f);
+  }
+  template <class E>
+  __device__ __forceinline__ void store(E* row, int v, const F8& f) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col(v, j) < H) store1(row + col(v, j), get8(f, j));
   }
   // The element type known at run time only (uniform over the launch).
   __device__ __forceinline__ F8 load(const void* row, int f32, int v) const {
@@ -197,95 +255,41 @@ struct Cols {
     else
       store(static_cast<uint16_t*>(base) + off, v, f);
   }
-
-  // Row m of `s` into its place in `stage`.
+  // Row m of `s` into its place in `stage`: the 16-byte units that the row
+  // touches.  Its neighbours' ends come along, but nothing past the last row's end.
   template <class E>
   __device__ __forceinline__ void fetch(unsigned char* stage, const RowSrc& s, int64_t m, int64_t M) const {
     const E* row = static_cast<const E*>(s.p) + m * s.ld;
-    unsigned char* dst = stage + s.off;
-    if constexpr (VEC) {
-      // 8 bf16: one unit per thread; 8 floats: two, in two planes
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        if (!in(v)) continue;
-        if constexpr (sizeof(E) == 2) {
-          cp16(dst + (v * T + t) * 16, row + col(v, 0));
-        } else {
-          cp16_l1(dst + (v * T + t) * 16, row + col(v, 0));
-          cp16_l1(dst + ((VPT + v) * T + t) * 16, row + col(v, 0) + 4);
-        }
-      }
-    } else {
-      // the 16-byte units that the row touches: its neighbours' ends come along,
-      // but nothing past the last row's end
-      const uintptr_t at = reinterpret_cast<uintptr_t>(row), lead = at & 15;
-      const uintptr_t end = at + ((M - 1 - m) * s.ld + H) * sizeof(E);
-      const int bytes = static_cast<int>(lead) + H * static_cast<int>(sizeof(E));
-      for (int u = t; u * 16 < bytes; u += T) {
-        const uintptr_t from = at - lead + u * 16;
-        cp16(dst + u * 16, reinterpret_cast<const void*>(from), end - from < 16 ? static_cast<int>(end - from) : 16);
-      }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row), lead = at & 15;
+    const uintptr_t end = at + ((M - 1 - m) * s.ld + H) * sizeof(E);
+    const int bytes = static_cast<int>(lead) + H * static_cast<int>(sizeof(E));
+    for (int u = t; u * 16 < bytes; u += T) {
+      const uintptr_t from = at - lead + u * 16;
+      cp16(smem_addr(stage + s.off) + u * 16, reinterpret_cast<const void*>(from),
+           end - from < 16 ? static_cast<int>(end - from) : 16);
     }
-  }
-  // VEC: the places of columns past H in a stage, which fetch() leaves alone.
-  template <class E>
-  __device__ __forceinline__ void clear(unsigned char* stage, const RowSrc& s) const {
-    if (!s.p) return;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-      if (!in(v))
-        for (int plane = 0; plane < static_cast<int>(sizeof(E)) / 2; ++plane)
-          *reinterpret_cast<uint4*>(stage + s.off + ((plane * VPT + v) * T + t) * 16) = make_uint4(0, 0, 0, 0);
   }
   // Group v of row m, from the stage that fetch() filled.
   template <class E>
   __device__ __forceinline__ F8 staged(const unsigned char* stage, const RowSrc& s, int64_t m, int v) const {
-    const unsigned char* src = stage + s.off;
-    if constexpr (VEC) {
-      const uint4 q = *reinterpret_cast<const uint4*>(src + (v * T + t) * 16);
-      if constexpr (sizeof(E) == 2) return unpack8(q);
-      const uint4 u = *reinterpret_cast<const uint4*>(src + ((VPT + v) * T + t) * 16);
-      return {{f2(__uint_as_float(q.x), __uint_as_float(q.y)), f2(__uint_as_float(q.z), __uint_as_float(q.w)),
-               f2(__uint_as_float(u.x), __uint_as_float(u.y)), f2(__uint_as_float(u.z), __uint_as_float(u.w))}};
-    } else {
-      const uintptr_t lead = reinterpret_cast<uintptr_t>(static_cast<const E*>(s.p) + m * s.ld) & 15;
-      return load(reinterpret_cast<const E*>(src + lead), v);
-    }
+    const uintptr_t lead = reinterpret_cast<uintptr_t>(static_cast<const E*>(s.p) + m * s.ld) & 15;
+    return load(reinterpret_cast<const E*>(stage + s.off + lead), v);
   }
 };
 
-__device__ __forceinline__ float sigmoid_f32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
-__device__ __forceinline__ F8 sigmoid8(const F8& g) {
-  float f[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = sigmoid_f32(get8(g, j));
-  return set8(f);
-}
-
-// The rows of a CTA, one after another.  VEC always has a ring; other rows have
-// one unless they are too long for it or their bases are not 16-byte aligned.
-template <class XT, class YT, int VPT, bool VEC, bool BWD>
+// The rows of a CTA, one after another, from a ring, or from memory where they are too
+// long for it or their bases are not 16-byte aligned.
+template <class XT, class YT, int VPT, bool BWD>
 struct Rows {
   const NormArgs& a;
-  const Cols<VPT, VEC>& c;
+  const Cols<VPT>& c;
   unsigned char* ring;
   unsigned char* cur;
   int put_stage = 0, stage = 0;
   int64_t put_row;
 
-  __device__ __forceinline__ bool ringed() const { return VEC || a.stages; }
-  __device__ __forceinline__ Rows(const NormArgs& a_, const Cols<VPT, VEC>& c_, unsigned char* ring_)
+  __device__ __forceinline__ Rows(const NormArgs& a_, const Cols<VPT>& c_, unsigned char* ring_)
       : a(a_), c(c_), ring(ring_), cur(ring_), put_row(blockIdx.x) {
-    if constexpr (VEC) {
-      for (int i = 0; i < a.stages; ++i) {
-        unsigned char* to = ring + i * a.stage_bytes;
-        c.template clear<XT>(to, a.dr);
-        c.template clear<XT>(to, a.x);
-        a.n_f32 ? c.template clear<float>(to, a.dn) : c.template clear<uint16_t>(to, a.dn);
-        c.template clear<YT>(to, a.y);
-        a.gate_f32 ? c.template clear<float>(to, a.gate) : c.template clear<uint16_t>(to, a.gate);
-      }
-    }
     for (int i = 0; i + 1 < a.stages; ++i) put();
   }
   __device__ __forceinline__ void put() {
@@ -303,20 +307,19 @@ struct Rows {
     cp_commit();
     put_stage = put_stage + 1 == a.stages ? 0 : put_stage + 1;
   }
-  // Makes the next row readable and sets off the row `stages - 1` further on.  The
-  // stage that it fills is the last row's: this thread's own part of it, or,
-  // read across threads, behind a barrier that they all reach after it.
+  // Makes the next row readable and sets off the row `stages - 1` further on, into
+  // the stage of the last row, which all threads have left behind at the barrier.
   __device__ __forceinline__ void next() {
-    if (!ringed()) return;
+    if (!a.stages) return;
     cp_wait(a.stages);
-    if constexpr (!VEC) __syncthreads();
+    __syncthreads();
     put();
     cur = ring + stage * a.stage_bytes;
     stage = stage + 1 == a.stages ? 0 : stage + 1;
   }
   template <class E>
   __device__ __forceinline__ F8 load(const RowSrc& s, int64_t m, int v) const {
-    if (ringed()) return c.template staged<E>(cur, s, m, v);
+    if (a.stages) return c.template staged<E>(cur, s, m, v);
     return c.load(static_cast<const E*>(s.p) + m * s.ld, v);
   }
   __device__ __forceinline__ F8 load(const RowSrc& s, int64_t m, int f32, int v) const {
@@ -326,8 +329,7 @@ struct Rows {
   __device__ __forceinline__ F8 gate(int64_t m, int v) const {
     if (a.gate_kind == E4B_GATE_FULL) return load(a.gate, m, a.gate_f32, v);
     if (a.gate_kind == E4B_GATE_CHANNEL) return c.load(a.vec_gate, a.gate_f32, v);
-    return fill8(a.gate_f32 ? load1(static_cast<const float*>(a.vec_gate) + m)
-                            : load1(static_cast<const uint16_t*>(a.vec_gate) + m));
+    return fill8(load1(a.vec_gate, m, a.gate_f32));
   }
 };
 

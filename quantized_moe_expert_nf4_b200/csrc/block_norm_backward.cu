@@ -4,15 +4,17 @@
 namespace e4b {
 namespace {
 
-template <class XT, class YT, int VPT, bool VEC>
-__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1) block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
+// Rows of any width, stride and base.
+template <class XT, class YT, int VPT>
+__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
+    block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
   // Buffers alternate by row: a row may have one sum only, and so no other
   // barrier before the next row's.
   __shared__ float red[2][2][3 * 16];
   const int T = blockDim.x;
-  const Cols<VPT, VEC> c{T, static_cast<int>(threadIdx.x), a.H};
-  Rows<XT, YT, VPT, VEC, true> rows(a, c, ring);
+  const Cols<VPT> c{T, static_cast<int>(threadIdx.x), a.H};
+  Rows<XT, YT, VPT, true> rows(a, c, ring);
   const bool has_y = a.y.p != nullptr, next = a.w_next != nullptr, post = a.w_post != nullptr;
   const int kind = a.gate_kind;
   const F2 offset = f2(a.offset);
@@ -81,12 +83,7 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1) block_nor
     if (!has_y) continue;
     float s2[2] = {lo(u0) + hi(u0), lo(u1) + hi(u1)};
     if (post || kind == E4B_GATE_TOKEN) row_sum<2>(s2, T, red[odd][1]);
-    if (kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0) {
-      if (a.gate_f32)
-        store1(static_cast<float*>(a.dgate) + m, s2[1]);
-      else
-        store1(static_cast<uint16_t*>(a.dgate) + m, s2[1]);
-    }
+    if (kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0) store1(a.dgate, m, a.gate_f32, s2[1]);
     if (!a.dy) continue;
     const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
 #pragma unroll
@@ -105,9 +102,168 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1) block_nor
   }
 }
 
+// Rows moved as vectors.  ALL: y, both weights, dr, dx and dy are there, the step
+// between two blocks in training; what each row would ask of them at run time
+// costs about a third of the kernel's instructions.
+template <class XT, class YT, int VPT, bool ALL>
+__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
+    block_norm_backward_vec_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float red[2][2][3 * 16];  // as above
+  const int T = blockDim.x;
+  const VecCols<VPT> c(T, threadIdx.x, a.H);
+  const bool has_y = ALL || a.y.p, next = ALL || a.w_next, post = ALL || a.w_post;
+  const bool has_dr = ALL || a.dr.p, has_dx = ALL || a.dx, has_dy = ALL || a.dy;
+  const int kind = a.gate_kind, stages = a.stages;
+  const int64_t step = gridDim.x;
+  const XT* r_p = static_cast<const XT*>(a.x.p) + blockIdx.x * a.x.ld;
+  const XT* dr_p = static_cast<const XT*>(a.dr.p) + blockIdx.x * a.dr.ld;
+  const YT* y_p = static_cast<const YT*>(a.y.p) + blockIdx.x * a.y.ld;
+  const unsigned char* dn_p = static_cast<const unsigned char*>(a.dn.p) + blockIdx.x * a.dn.ld * (a.n_f32 ? 4 : 2);
+  const unsigned char* g_p = static_cast<const unsigned char*>(a.gate.p) + blockIdx.x * a.gate.ld * (a.gate_f32 ? 4 : 2);
+  const uint32_t ring_u = smem_addr(ring) + threadIdx.x * 16;
+  const unsigned char* ring_p = ring + threadIdx.x * 16;
+  int64_t put_row = blockIdx.x;
+  int put_stage = 0, stage = 0;
+  // A thread reads its own places only, so that filling the last row's stage needs no barrier.
+  auto put = [&]() {
+    if (put_row < a.M) {
+      const uint32_t to = ring_u + put_stage * a.stage_bytes;
+      if (next) {
+        c.fetch(to + a.x.off, r_p);
+        if (a.n_f32)
+          c.fetch(to + a.dn.off, reinterpret_cast<const float*>(dn_p));
+        else
+          c.fetch(to + a.dn.off, reinterpret_cast<const uint16_t*>(dn_p));
+        r_p += step * a.x.ld;
+        dn_p += step * a.dn.ld * (a.n_f32 ? 4 : 2);
+      }
+      if (has_y) {
+        c.fetch(to + a.y.off, y_p);
+        y_p += step * a.y.ld;
+      }
+      if (has_dr) {
+        c.fetch(to + a.dr.off, dr_p);
+        dr_p += step * a.dr.ld;
+      }
+      if (kind == E4B_GATE_FULL) {
+        if (a.gate_f32)
+          c.fetch(to + a.gate.off, reinterpret_cast<const float*>(g_p));
+        else
+          c.fetch(to + a.gate.off, reinterpret_cast<const uint16_t*>(g_p));
+        g_p += step * a.gate.ld * (a.gate_f32 ? 4 : 2);
+      }
+      put_row += step;
+    }
+    cp_commit();
+    put_stage = put_stage + 1 == stages ? 0 : put_stage + 1;
+  };
+  for (int i = 0; i + 1 < stages; ++i) put();
+  const F2 offset = f2(a.offset);
+  F8 s_post[VPT], s_next[VPT], s_gate[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) s_post[v] = s_next[v] = s_gate[v] = zero8();
+  int odd = 0;
+  XT* dx_p = static_cast<XT*>(a.dx) + blockIdx.x * a.lddx;
+  YT* dy_p = static_cast<YT*>(a.dy) + blockIdx.x * a.lddy;
+  for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, dx_p += step * a.lddx, dy_p += step * a.lddy) {
+    cp_wait(stages);
+    put();
+    const unsigned char* cur = ring_p + stage * a.stage_bytes;
+    stage = stage + 1 == stages ? 0 : stage + 1;
+    auto load_dn = [&](int v) {
+      return a.n_f32 ? c.template staged<float>(cur + a.dn.off, v) : c.template staged<uint16_t>(cur + a.dn.off, v);
+    };
+    float s1[3] = {0.0f, 0.0f, 0.0f};  // sums of r^2, h * r, y^2
+    F8 h[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const F2 z = f2(0.0f);
+      if (has_y) {
+        const F8 y = c.template staged<YT>(cur + a.y.off, v);
+        const F2 q = dot8(y, y, z);
+        s1[2] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+      }
+      if (next) {
+        const F8 r = c.template staged<XT>(cur + a.x.off, v);
+        h[v] = load_dn(v) * (c.vector(a.w_next, a.w_f32, v) + offset);
+        const F2 q = dot8(r, r, z), u = dot8(h[v], r, z);
+        s1[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+        s1[1] += c.in[v] ? lo(u) + hi(u) : 0.0f;
+      }
+    }
+    row_sum<3>(s1, T, red[odd][0]);
+    const float rstd_r = rsqrtf(s1[0] * a.inv_h + a.eps), rstd_y = post ? rsqrtf(s1[2] * a.inv_h + a.eps) : 1.0f;
+    const float mean_r = s1[1] * rstd_r * a.inv_h;  // mean(h * rhat)
+    F8 k[VPT];
+    float s2[2] = {0.0f, 0.0f};  // sums of k * yhat, d * z * slope
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      F8 d = has_dr ? c.template staged<XT>(cur + a.dr.off, v) : zero8();
+      if (next) {
+        const F8 hat = c.template staged<XT>(cur + a.x.off, v) * f2(rstd_r);
+        s_next[v] = fma8(load_dn(v), hat, s_next[v]);
+        d = fma8(fma8(hat, f2(-mean_r), h[v]), f2(rstd_r), d);
+      }
+      if (has_dx) c.store(dx_p, v, d);
+      if (!has_y) continue;
+      const F8 hat = c.template staged<YT>(cur + a.y.off, v) * f2(rstd_y);
+      const F8 w = post ? c.vector(a.w_post, a.w_f32, v) + offset : fill8(1.0f);
+      F8 dz = d * f2(a.scale);
+      if (kind != E4B_GATE_NONE) {
+        F8 f = kind == E4B_GATE_CHANNEL ? c.vector(a.vec_gate, a.gate_f32, v)
+               : kind == E4B_GATE_TOKEN ? fill8(load1(a.vec_gate, m, a.gate_f32))
+               : a.gate_f32             ? c.template staged<float>(cur + a.gate.off, v)
+                                        : c.template staged<uint16_t>(cur + a.gate.off, v);
+        F8 dg = dz * (hat * w);
+        if (a.sigmoid) {
+          f = sigmoid8(f);
+          dg = dg * (f * fma8(f, f2(-1.0f), fill8(1.0f)));
+        }
+        dz = dz * f;
+        if (kind == E4B_GATE_CHANNEL) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s_gate[v].p[j] = s_gate[v].p[j] + dg.p[j];
+        } else if (kind == E4B_GATE_TOKEN) {
+          const F2 q = (dg.p[0] + dg.p[1]) + (dg.p[2] + dg.p[3]);
+          s2[1] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+        } else if (a.dgate) {
+          if (a.gate_f32)
+            c.store(static_cast<float*>(a.dgate) + m * a.H, v, dg);
+          else
+            c.store(static_cast<uint16_t*>(a.dgate) + m * a.H, v, dg);
+        }
+      }
+      s_post[v] = fma8(dz, hat, s_post[v]);
+      k[v] = dz * w;
+      const F2 q = dot8(k[v], hat, f2(0.0f));
+      s2[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+    }
+    if (!has_y) continue;
+    if (post || kind == E4B_GATE_TOKEN) row_sum<2>(s2, T, red[odd][1]);
+    if (kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0) store1(a.dgate, m, a.gate_f32, s2[1]);
+    if (!has_dy) continue;
+    const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      c.store(dy_p, v, fma8(c.template staged<YT>(cur + a.y.off, v), f2(-mean_y), k[v]) * f2(rstd_y));
+  }
+  const int64_t plane = static_cast<int64_t>(a.parts) * a.H;
+  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.H;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (post) c.store(part, v, s_post[v]);
+    if (next) c.store(part + plane, v, s_next[v]);
+    if (kind == E4B_GATE_CHANNEL) c.store(part + 2 * plane, v, s_gate[v]);
+  }
+}
+
 template <class XT, class YT, int VPT>
 cudaError_t launch_groups(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  auto* kernel = vec ? block_norm_backward_kernel<XT, YT, VPT, true> : block_norm_backward_kernel<XT, YT, VPT, false>;
+  const bool all = a.y.p && a.w_next && a.w_post && a.dr.p && a.dx && a.dy;
+  auto* kernel = !vec  ? block_norm_backward_kernel<XT, YT, VPT>
+                 : all ? block_norm_backward_vec_kernel<XT, YT, VPT, true>
+                       : block_norm_backward_vec_kernel<XT, YT, VPT, false>;
   const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
   kernel<<<s.grid, s.T, smem, stream>>>(a);
