@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
   extern __shared__ __align__(16) unsigned char ring[];
   // Buffers alternate by row: a row may have one sum only, and so no other
   // barrier before the next row's.
-  __shared__ float red[2][2][16];
+  __shared__ float red[2][2][64];
   const int T = blockDim.x;
   const Cols<VPT> c{T, static_cast<int>(threadIdx.x), a.H};
   Rows<XT, YT, VPT, false> rows(a, c, ring);
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
         } else {
           r[v] = fma8(z[v], f2(1.0f), r[v]);
         }
-        c.store(static_cast<XT*>(a.r) + m * a.ldr, v, r[v]);
+        c.store(reinterpret_cast<XT*>(static_cast<unsigned char*>(a.r.p) + m * a.r.row), v, r[v]);
       }
     } else {
 #pragma unroll
@@ -91,25 +91,24 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
     const F2 rstd = f2(rsqrtf(ss[0] * a.inv_h + a.eps));
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      c.store(a.n, m * a.ldn, a.n_f32, v, r[v] * rstd * (c.load(a.w_next, a.w_f32, v) + offset));
+      c.store(static_cast<unsigned char*>(a.n.p) + m * a.n.row, 0, a.n_f32, v, r[v] * rstd * (c.load(a.w_next, a.w_f32, v) + offset));
   }
 }
 
 // Rows moved as vectors.  ALL: y and both weights are there, the step between two
 // blocks.
 template <class XT, class YT, int VPT, bool ALL>
-__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2 : 1)
+__global__ void __launch_bounds__(norm_threads(VPT), VPT < 4 ? 2 : 1)
     block_norm_forward_vec_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float red[2][2][16];  // as above
+  __shared__ float red[2][2][64];  // as above
   const int T = blockDim.x;
   const VecCols<VPT> c(T, threadIdx.x, a.H);
   const bool has_y = ALL || a.y.p, next = ALL || a.w_next, post = ALL || a.w_post;
   const int kind = a.gate_kind, stages = a.stages;
-  const int64_t step = gridDim.x;
-  const XT* x_p = static_cast<const XT*>(a.x.p) + blockIdx.x * a.x.ld;
-  const YT* y_p = static_cast<const YT*>(a.y.p) + blockIdx.x * a.y.ld;
-  const unsigned char* g_p = static_cast<const unsigned char*>(a.gate.p) + blockIdx.x * a.gate.ld * (a.gate_f32 ? 4 : 2);
+  const int step = static_cast<int>(gridDim.x);
+  auto row_of = [&](const RowSrc& t) { return static_cast<const unsigned char*>(t.p) + blockIdx.x * t.row; };
+  const unsigned char *x_p = row_of(a.x), *y_p = row_of(a.y), *g_p = row_of(a.gate);
   const uint32_t ring_u = smem_addr(ring) + threadIdx.x * 16;
   const unsigned char* ring_p = ring + threadIdx.x * 16;
   int64_t put_row = blockIdx.x;
@@ -118,18 +117,18 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
   auto put = [&]() {
     if (put_row < a.M) {
       const uint32_t to = ring_u + put_stage * a.stage_bytes;
-      c.fetch(to + a.x.off, x_p);
-      x_p += step * a.x.ld;
+      c.template fetch<XT>(to + a.x.off, x_p);
+      x_p += a.x.step;
       if (has_y) {
-        c.fetch(to + a.y.off, y_p);
-        y_p += step * a.y.ld;
+        c.template fetch<YT>(to + a.y.off, y_p);
+        y_p += a.y.step;
       }
       if (kind == E4B_GATE_FULL) {
         if (a.gate_f32)
-          c.fetch(to + a.gate.off, reinterpret_cast<const float*>(g_p));
+          c.template fetch<float>(to + a.gate.off, g_p);
         else
-          c.fetch(to + a.gate.off, reinterpret_cast<const uint16_t*>(g_p));
-        g_p += step * a.gate.ld * (a.gate_f32 ? 4 : 2);
+          c.template fetch<uint16_t>(to + a.gate.off, g_p);
+        g_p += a.gate.step;
       }
       put_row += step;
     }
@@ -138,10 +137,20 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
   };
   for (int i = 0; i + 1 < stages; ++i) put();
   const F2 offset = f2(a.offset);
-  XT* r_p = static_cast<XT*>(a.r) + blockIdx.x * a.ldr;
-  unsigned char* n_p = static_cast<unsigned char*>(a.n) + blockIdx.x * a.ldn * (a.n_f32 ? 4 : 2);
+  // One group per thread: its weights and channel gate stay in registers.
+  constexpr bool kHold = VPT == 1;
+  F8 hold_post, hold_next, hold_gate;
+  if constexpr (kHold) {
+    if (post) hold_post = c.vector(a.w_post, a.w_f32, 0) + offset;
+    if (next) hold_next = c.vector(a.w_next, a.w_f32, 0) + offset;
+    if (kind == E4B_GATE_CHANNEL) hold_gate = c.vector(a.vec_gate, a.gate_f32, 0);
+  }
+  auto w_post = [&](int v) { return kHold ? hold_post : c.vector(a.w_post, a.w_f32, v) + offset; };
+  auto w_next = [&](int v) { return kHold ? hold_next : c.vector(a.w_next, a.w_f32, v) + offset; };
+  unsigned char* r_p = static_cast<unsigned char*>(a.r.p) + blockIdx.x * a.r.row;
+  unsigned char* n_p = static_cast<unsigned char*>(a.n.p) + blockIdx.x * a.n.row;
   int odd = 0;
-  for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, r_p += step * a.ldr, n_p += step * a.ldn * (a.n_f32 ? 4 : 2)) {
+  for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, r_p += a.r.step, n_p += a.n.step) {
     cp_wait(stages);
     put();
     const unsigned char* cur = ring_p + stage * a.stage_bytes;
@@ -165,9 +174,9 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         F8 z = c.template staged<YT>(cur + a.y.off, v) * f2(factor);
-        if (post) z = z * (c.vector(a.w_post, a.w_f32, v) + offset);
+        if (post) z = z * w_post(v);
         if (kind != E4B_GATE_NONE) {
-          F8 f = kind == E4B_GATE_CHANNEL ? c.vector(a.vec_gate, a.gate_f32, v)
+          F8 f = kind == E4B_GATE_CHANNEL ? (kHold ? hold_gate : c.vector(a.vec_gate, a.gate_f32, v))
                  : kind == E4B_GATE_TOKEN ? fill8(load1(a.vec_gate, m, a.gate_f32))
                  : a.gate_f32             ? c.template staged<float>(cur + a.gate.off, v)
                                           : c.template staged<uint16_t>(cur + a.gate.off, v);
@@ -176,7 +185,7 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
         } else {
           r[v] = fma8(z, f2(1.0f), r[v]);
         }
-        c.store(r_p, v, r[v]);
+        c.template store<XT>(r_p, v, r[v]);
       }
     }
     if (!next) continue;
@@ -190,11 +199,11 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2
     const F2 rstd = f2(rsqrtf(ss[0] * a.inv_h + a.eps));
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const F8 n = r[v] * rstd * (c.vector(a.w_next, a.w_f32, v) + offset);
+      const F8 n = r[v] * rstd * w_next(v);
       if (a.n_f32)
-        c.store(reinterpret_cast<float*>(n_p), v, n);
+        c.template store<float>(n_p, v, n);
       else
-        c.store(reinterpret_cast<uint16_t*>(n_p), v, n);
+        c.template store<uint16_t>(n_p, v, n);
     }
   }
 }
@@ -218,14 +227,14 @@ cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaSt
   return launch_groups<XT, YT, 4>(a, s, vec, stream);
 }
 
-// out[q][col] = sum over parts of partial[q][part][col], in a fixed order: 16
-// threads of a column take every 16th part, then are added in order.
+// out[q][col] = sum over parts of partial[q][part][col], in a fixed order: 32
+// threads of a column take every 32nd part, then are added in order.
 struct ReduceArgs {
   const float* partial;
   float* out[3];
   int parts, H;
 };
-constexpr int kRedCols = 32, kRedLanes = 16;
+constexpr int kRedCols = 32, kRedLanes = 32;
 
 __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel(ReduceArgs a) {
   float* out = a.out[blockIdx.y];
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel
   float sum = 0.0f;
   if (col < a.H) {
     const float* p = a.partial + static_cast<int64_t>(blockIdx.y) * a.parts * a.H + col;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.y; i < a.parts; i += kRedLanes) sum += p[static_cast<int64_t>(i) * a.H];
   }
   s[threadIdx.y][threadIdx.x] = sum;
@@ -259,7 +268,7 @@ NormShape norm_shape(int64_t M, int H, int threads_per_sm) {
   s.grid = static_cast<int>(std::min<int64_t>(M, kSms * per_sm));
   return s;
 }
-constexpr int kForwardThreads = 1152, kBackwardThreads = 768;  // per SM
+constexpr int kForwardThreads = 768, kBackwardThreads = 768;  // per SM
 
 // How a call's rows can be moved: as vectors of 8 columns, or else in units of 16 bytes.
 struct Moves {
@@ -269,6 +278,7 @@ struct Moves {
 // The ring: as many stages (2 to 4) as leave room for the SM's other CTAs, or, of
 // rows too long for that, none.  Returns whether rows are moved as vectors.
 bool plan_ring(NormArgs* a, const NormShape& s, const Moves& moves, bool x_f32, bool y_f32, int threads_per_sm) {
+  for (RowDst* d : {&a->r, &a->n, &a->dx, &a->dy}) d->step = d->row * s.grid;
   constexpr uint32_t kRoom = 216 * 1024;
   const int ctas = std::min(16, std::max(1, threads_per_sm / s.T));
   for (const bool vec : {true, false}) {
@@ -276,6 +286,8 @@ bool plan_ring(NormArgs* a, const NormShape& s, const Moves& moves, bool x_f32, 
     uint32_t off = 0;
     auto place = [&](RowSrc* r, bool f32) {
       if (!r->p) return;
+      r->row = r->ld * (f32 ? 4 : 2);
+      r->step = r->row * s.grid;
       r->off = off;
       off += vec ? static_cast<uint32_t>(s.T * s.vpt * 8 * (f32 ? 4 : 2))
                  : static_cast<uint32_t>(align_up(static_cast<size_t>(a->H) * (f32 ? 4 : 2), 16) + 16);
@@ -293,6 +305,7 @@ bool plan_ring(NormArgs* a, const NormShape& s, const Moves& moves, bool x_f32, 
   return false;
 }
 
+int64_t size_of(int dtype) { return dtype == E4B_F32 ? 4 : 2; }
 bool is_dtype(int d) { return d == E4B_F32 || d == E4B_BF16; }
 bool on_element(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == E4B_F32 ? 3u : 1u)) == 0;
@@ -337,7 +350,7 @@ e4b_status check_rows(const char* name, const void* p, int dtype, int64_t ld, in
 NormArgs norm_args(const e4b_block_norm* p, int64_t M, const void* y, int64_t ldy, const void* gate, e4b_gate_kind kind,
                    e4b_dtype gate_dtype, e4b_dtype n_dtype) {
   NormArgs a{};
-  a.y = {y, ldy, 0};
+  a.y = {y, ldy};
   (kind == E4B_GATE_FULL ? a.gate.p : a.vec_gate) = gate;
   a.gate.ld = p->H;
   a.w_post = p->w_post;
@@ -403,11 +416,11 @@ e4b_status e4b_block_norm_forward(const void* x, e4b_dtype x_dtype, int64_t ldx,
   }
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   NormArgs a = norm_args(norm, M, y, ldy, gate, gate_kind, gate_dtype, n_dtype);
-  a.x = {x, ldx, 0};
-  a.r = r;
-  a.n = n;
-  a.ldr = ldr;
-  a.ldn = ldn;
+  a.x = {x, ldx};
+  a.r.p = r;
+  a.r.row = ldr * size_of(x_dtype);
+  a.n.p = n;
+  a.n.row = ldn * size_of(n_dtype);
   const NormShape s = norm_shape(M, a.H, kForwardThreads);
   const bool x_f32 = x_dtype == E4B_F32, y_f32 = y && y_dtype == E4B_F32;
   const bool vec = plan_ring(&a, s, moves, x_f32, y_f32, kForwardThreads);
@@ -456,15 +469,15 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
   if (e4b_status s = check_sm100(); s != E4B_OK) return s;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   NormArgs a = norm_args(norm, M, y, ldy, gate, gate_kind, gate_dtype, n_dtype);
-  a.dr = {dr, lddr, 0};
-  a.dn = {dn, lddn, 0};
-  if (norm->w_next) a.x = {r, ldr, 0};
-  a.dx = dx;
-  a.dy = dy;
+  a.dr = {dr, lddr};
+  a.dn = {dn, lddn};
+  if (norm->w_next) a.x = {r, ldr};
+  a.dx.p = dx;
+  a.dx.row = lddx * size_of(x_dtype);
+  a.dy.p = dy;
+  a.dy.row = lddy * size_of(y_dtype);
   a.dgate = dgate;
   a.partial = static_cast<float*>(workspace);
-  a.lddx = lddx;
-  a.lddy = lddy;
   bool vec = false;
   if (M > 0) {
     const NormShape s = norm_shape(M, a.H, kBackwardThreads);

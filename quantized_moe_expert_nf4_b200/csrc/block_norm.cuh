@@ -15,16 +15,22 @@ struct RowSrc {
   const void* p;
   int64_t ld;
   uint32_t off;
+  int64_t row, step;  // bytes from a row to the next, and to the same CTA's next
+};
+// One that it writes.
+struct RowDst {
+  void* p;
+  int64_t row, step;
 };
 
 struct NormArgs {
   RowSrc x, y, gate;                 // x: also r of the backward; gate: E4B_GATE_FULL's rows
   RowSrc dr, dn;                     // backward
   const void *vec_gate, *w_post, *w_next;  // vec_gate: channel or token gate
-  void *r, *n;                       // forward
-  void *dx, *dy, *dgate;             // backward
+  RowDst r, n;                       // forward
+  RowDst dx, dy;                     // backward
+  void* dgate;
   float* partial;                    // backward: [3][parts][H] column sums (w_post, w_next, channel gate)
-  int64_t ldr, ldn, lddx, lddy;      // of the outputs
   int64_t M;
   int H, parts;
   int stages;                        // of the ring; 0: rows are read from memory directly
@@ -119,9 +125,13 @@ __device__ __forceinline__ F8 unpack8(uint4 q) {
            f2(__uint_as_float(q.z << 16), __uint_as_float(q.z & 0xffff0000u)),
            f2(__uint_as_float(q.w << 16), __uint_as_float(q.w & 0xffff0000u))}};
 }
-__device__ __forceinline__ F8 join8(float4 a, float4 b) { return {{f2(a.x, a.y), f2(a.z, a.w), f2(b.x, b.y), f2(b.z, b.w)}}; }
+// A 32-byte load (of data that no kernel writes meanwhile).
 __device__ __forceinline__ F8 load8(const float* p) {
-  return join8(*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4));
+  float v[8];
+  asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+      : "l"(p));
+  return {{f2(v[0], v[1]), f2(v[2], v[3]), f2(v[4], v[5]), f2(v[6], v[7])}};
 }
 __device__ __forceinline__ F8 load8(const uint16_t* p) { return unpack8(*reinterpret_cast<const uint4*>(p)); }
 // One 32-byte store: two of 16 bytes would each write half of every sector.
@@ -194,10 +204,10 @@ struct VecCols {
   // Into this thread's places of a ring stage (`dst`: its unit of plane 0) from a
   // row: 8 bf16 are one unit, 8 floats two, in two planes.
   template <class E>
-  __device__ __forceinline__ void fetch(uint32_t dst, const E* row) const {
+  __device__ __forceinline__ void fetch(uint32_t dst, const unsigned char* row) const {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const E* src = row + col[v];
+      const E* src = reinterpret_cast<const E*>(row) + col[v];
       if constexpr (sizeof(E) == 2) {
         cp16(dst + v * T16, src);
       } else {
@@ -219,8 +229,8 @@ struct VecCols {
     return f32 ? load8(static_cast<const float*>(p) + col[v]) : load8(static_cast<const uint16_t*>(p) + col[v]);
   }
   template <class E>
-  __device__ __forceinline__ void store(E* row, int v, const F8& f) const {
-    if (in[v]) store8(row + col[v], f);
+  __device__ __forceinline__ void store(unsigned char* row, int v, const F8& f) const {
+    if (in[v]) store8(reinterpret_cast<E*>(row) + col[v], f);
   }
 };
 
@@ -333,27 +343,59 @@ struct Rows {
   }
 };
 
-// Sums of up to three values over the CTA's T threads (a multiple of 32, at most
-// 512).  One barrier above one warp: a caller that sums again passes another buffer.
+// Sums of one to three values over the CTA's T threads (a multiple of 32, at most
+// 512), to every thread.  Several values share the shuffles: a warp's halves (or
+// quarters) first exchange the values that each will add up (11 shuffles for two
+// and 12 for three instead of 18 and 27).  One barrier above one warp: a caller
+// that sums again passes another buffer of 64 floats.
+__device__ __forceinline__ float add_xor(float v, int o) { return v + __shfl_xor_sync(0xffffffffu, v, o); }
+
 template <int NV>
 __device__ __forceinline__ void row_sum(float v[NV], int T, float* red) {
+  const int lane = threadIdx.x & 31, warps = T >> 5, warp = threadIdx.x >> 5;
+  if constexpr (NV == 1) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1) v[0] = add_xor(v[0], o);
+    if (T == 32) return;
+    if (lane == 0) red[warp] = v[0];
+    __syncthreads();
+    v[0] = (lane & 15) < warps ? red[lane & 15] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (T == 32) return;
-  const int lane = threadIdx.x & 31, warps = T >> 5;
-  if (lane == 0)
+    for (int o = 8; o > 0; o >>= 1) v[0] = add_xor(v[0], o);
+  } else if constexpr (NV == 2) {
+    // lanes 0-15 add up value 0, lanes 16-31 value 1
+    const bool up = lane & 16;
+    float s = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) red[i * 16 + (threadIdx.x >> 5)] = v[i];
-  __syncthreads();
-  // every warp adds the warps' sums alike: lanes w and w + 16 hold warp w's
+    for (int o = 8; o > 0; o >>= 1) s = add_xor(s, o);
+    if (T > 32) {
+      if ((lane & 15) == 0) red[(lane >> 4) * 16 + warp] = s;
+      __syncthreads();
+      s = (lane & 15) < warps ? red[lane] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = (lane & 15) < warps ? red[i * 16 + (lane & 15)] : 0.0f;
+      for (int o = 8; o > 0; o >>= 1) s = add_xor(s, o);
+    }
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+    v[1] = __shfl_sync(0xffffffffu, s, 16);
+  } else {
+    // lanes 8 i .. 8 i + 7 add up value i (the fourth is none)
+    const bool up = lane & 16, odd = lane & 8;
+    const float s0 = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+    const float s1 = (up ? 0.0f : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : 0.0f, 16);
+    float s = (odd ? s1 : s0) + __shfl_xor_sync(0xffffffffu, odd ? s0 : s1, 8);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
+    for (int o = 4; o > 0; o >>= 1) s = add_xor(s, o);
+    if (T > 32) {
+      if ((lane & 7) == 0) red[(lane >> 3) * 16 + warp] = s;
+      __syncthreads();
+      const int w = lane & 7, i = (lane >> 3) * 16;
+      s = (w < warps ? red[i + w] : 0.0f) + (w + 8 < warps ? red[i + w + 8] : 0.0f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      for (int o = 4; o > 0; o >>= 1) s = add_xor(s, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = __shfl_sync(0xffffffffu, s, 8 * i);
+  }
 }
 
 }  // namespace e4b

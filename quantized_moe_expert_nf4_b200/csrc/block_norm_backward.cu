@@ -11,7 +11,7 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
   extern __shared__ __align__(16) unsigned char ring[];
   // Buffers alternate by row: a row may have one sum only, and so no other
   // barrier before the next row's.
-  __shared__ float red[2][2][3 * 16];
+  __shared__ float red[2][2][64];
   const int T = blockDim.x;
   const Cols<VPT> c{T, static_cast<int>(threadIdx.x), a.H};
   Rows<XT, YT, VPT, true> rows(a, c, ring);
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
         s_next[v] = fma8(dn, hat, s_next[v]);
         d = fma8(fma8(hat, f2(-mean_r), h), f2(rstd_r), d);
       }
-      if (a.dx) c.store(static_cast<XT*>(a.dx) + m * a.lddx, v, d);
+      if (a.dx.p) c.store(reinterpret_cast<XT*>(static_cast<unsigned char*>(a.dx.p) + m * a.dx.row), v, d);
       if (!has_y) continue;
       const F8 hat = rows.template load<YT>(a.y, m, v) * f2(rstd_y);
       const F8 w = post ? c.load(a.w_post, a.w_f32, v) + offset : fill8(1.0f);
@@ -84,12 +84,13 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     float s2[2] = {lo(u0) + hi(u0), lo(u1) + hi(u1)};
     if (post || kind == E4B_GATE_TOKEN) row_sum<2>(s2, T, red[odd][1]);
     if (kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0) store1(a.dgate, m, a.gate_f32, s2[1]);
-    if (!a.dy) continue;
+    if (!a.dy.p) continue;
     const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const F8 y = rows.template load<YT>(a.y, m, v);
-      c.store(static_cast<YT*>(a.dy) + m * a.lddy, v, fma8(y, f2(-mean_y), k[v]) * f2(rstd_y));
+      c.store(reinterpret_cast<YT*>(static_cast<unsigned char*>(a.dy.p) + m * a.dy.row), v,
+              fma8(y, f2(-mean_y), k[v]) * f2(rstd_y));
     }
   }
   const int64_t plane = static_cast<int64_t>(a.parts) * a.H;
@@ -109,18 +110,15 @@ template <class XT, class YT, int VPT, bool ALL>
 __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     block_norm_backward_vec_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float red[2][2][3 * 16];  // as above
+  __shared__ float red[2][2][64];  // as above
   const int T = blockDim.x;
   const VecCols<VPT> c(T, threadIdx.x, a.H);
   const bool has_y = ALL || a.y.p, next = ALL || a.w_next, post = ALL || a.w_post;
-  const bool has_dr = ALL || a.dr.p, has_dx = ALL || a.dx, has_dy = ALL || a.dy;
+  const bool has_dr = ALL || a.dr.p, has_dx = ALL || a.dx.p, has_dy = ALL || a.dy.p;
   const int kind = a.gate_kind, stages = a.stages;
-  const int64_t step = gridDim.x;
-  const XT* r_p = static_cast<const XT*>(a.x.p) + blockIdx.x * a.x.ld;
-  const XT* dr_p = static_cast<const XT*>(a.dr.p) + blockIdx.x * a.dr.ld;
-  const YT* y_p = static_cast<const YT*>(a.y.p) + blockIdx.x * a.y.ld;
-  const unsigned char* dn_p = static_cast<const unsigned char*>(a.dn.p) + blockIdx.x * a.dn.ld * (a.n_f32 ? 4 : 2);
-  const unsigned char* g_p = static_cast<const unsigned char*>(a.gate.p) + blockIdx.x * a.gate.ld * (a.gate_f32 ? 4 : 2);
+  const int step = static_cast<int>(gridDim.x);
+  auto row_of = [&](const RowSrc& t) { return static_cast<const unsigned char*>(t.p) + blockIdx.x * t.row; };
+  const unsigned char *r_p = row_of(a.x), *dr_p = row_of(a.dr), *y_p = row_of(a.y), *dn_p = row_of(a.dn), *g_p = row_of(a.gate);
   const uint32_t ring_u = smem_addr(ring) + threadIdx.x * 16;
   const unsigned char* ring_p = ring + threadIdx.x * 16;
   int64_t put_row = blockIdx.x;
@@ -130,28 +128,28 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     if (put_row < a.M) {
       const uint32_t to = ring_u + put_stage * a.stage_bytes;
       if (next) {
-        c.fetch(to + a.x.off, r_p);
+        c.template fetch<XT>(to + a.x.off, r_p);
         if (a.n_f32)
-          c.fetch(to + a.dn.off, reinterpret_cast<const float*>(dn_p));
+          c.template fetch<float>(to + a.dn.off, dn_p);
         else
-          c.fetch(to + a.dn.off, reinterpret_cast<const uint16_t*>(dn_p));
-        r_p += step * a.x.ld;
-        dn_p += step * a.dn.ld * (a.n_f32 ? 4 : 2);
+          c.template fetch<uint16_t>(to + a.dn.off, dn_p);
+        r_p += a.x.step;
+        dn_p += a.dn.step;
       }
       if (has_y) {
-        c.fetch(to + a.y.off, y_p);
-        y_p += step * a.y.ld;
+        c.template fetch<YT>(to + a.y.off, y_p);
+        y_p += a.y.step;
       }
       if (has_dr) {
-        c.fetch(to + a.dr.off, dr_p);
-        dr_p += step * a.dr.ld;
+        c.template fetch<XT>(to + a.dr.off, dr_p);
+        dr_p += a.dr.step;
       }
       if (kind == E4B_GATE_FULL) {
         if (a.gate_f32)
-          c.fetch(to + a.gate.off, reinterpret_cast<const float*>(g_p));
+          c.template fetch<float>(to + a.gate.off, g_p);
         else
-          c.fetch(to + a.gate.off, reinterpret_cast<const uint16_t*>(g_p));
-        g_p += step * a.gate.ld * (a.gate_f32 ? 4 : 2);
+          c.template fetch<uint16_t>(to + a.gate.off, g_p);
+        g_p += a.gate.step;
       }
       put_row += step;
     }
@@ -164,9 +162,9 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
 #pragma unroll
   for (int v = 0; v < VPT; ++v) s_post[v] = s_next[v] = s_gate[v] = zero8();
   int odd = 0;
-  XT* dx_p = static_cast<XT*>(a.dx) + blockIdx.x * a.lddx;
-  YT* dy_p = static_cast<YT*>(a.dy) + blockIdx.x * a.lddy;
-  for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, dx_p += step * a.lddx, dy_p += step * a.lddy) {
+  unsigned char* dx_p = static_cast<unsigned char*>(a.dx.p) + blockIdx.x * a.dx.row;
+  unsigned char* dy_p = static_cast<unsigned char*>(a.dy.p) + blockIdx.x * a.dy.row;
+  for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, dx_p += a.dx.step, dy_p += a.dy.step) {
     cp_wait(stages);
     put();
     const unsigned char* cur = ring_p + stage * a.stage_bytes;
@@ -205,7 +203,7 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
         s_next[v] = fma8(load_dn(v), hat, s_next[v]);
         d = fma8(fma8(hat, f2(-mean_r), h[v]), f2(rstd_r), d);
       }
-      if (has_dx) c.store(dx_p, v, d);
+      if (has_dx) c.template store<XT>(dx_p, v, d);
       if (!has_y) continue;
       const F8 hat = c.template staged<YT>(cur + a.y.off, v) * f2(rstd_y);
       const F8 w = post ? c.vector(a.w_post, a.w_f32, v) + offset : fill8(1.0f);
@@ -228,10 +226,11 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
           const F2 q = (dg.p[0] + dg.p[1]) + (dg.p[2] + dg.p[3]);
           s2[1] += c.in[v] ? lo(q) + hi(q) : 0.0f;
         } else if (a.dgate) {
+          unsigned char* row = static_cast<unsigned char*>(a.dgate) + m * a.gate.row;
           if (a.gate_f32)
-            c.store(static_cast<float*>(a.dgate) + m * a.H, v, dg);
+            c.template store<float>(row, v, dg);
           else
-            c.store(static_cast<uint16_t*>(a.dgate) + m * a.H, v, dg);
+            c.template store<uint16_t>(row, v, dg);
         }
       }
       s_post[v] = fma8(dz, hat, s_post[v]);
@@ -246,21 +245,21 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      c.store(dy_p, v, fma8(c.template staged<YT>(cur + a.y.off, v), f2(-mean_y), k[v]) * f2(rstd_y));
+      c.template store<YT>(dy_p, v, fma8(c.template staged<YT>(cur + a.y.off, v), f2(-mean_y), k[v]) * f2(rstd_y));
   }
   const int64_t plane = static_cast<int64_t>(a.parts) * a.H;
-  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.H;
+  auto part = [&](int q) { return reinterpret_cast<unsigned char*>(a.partial + q * plane + static_cast<int64_t>(blockIdx.x) * a.H); };
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    if (post) c.store(part, v, s_post[v]);
-    if (next) c.store(part + plane, v, s_next[v]);
-    if (kind == E4B_GATE_CHANNEL) c.store(part + 2 * plane, v, s_gate[v]);
+    if (post) c.template store<float>(part(0), v, s_post[v]);
+    if (next) c.template store<float>(part(1), v, s_next[v]);
+    if (kind == E4B_GATE_CHANNEL) c.template store<float>(part(2), v, s_gate[v]);
   }
 }
 
 template <class XT, class YT, int VPT>
 cudaError_t launch_groups(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  const bool all = a.y.p && a.w_next && a.w_post && a.dr.p && a.dx && a.dy;
+  const bool all = a.y.p && a.w_next && a.w_post && a.dr.p && a.dx.p && a.dy.p;
   auto* kernel = !vec  ? block_norm_backward_kernel<XT, YT, VPT>
                  : all ? block_norm_backward_vec_kernel<XT, YT, VPT, true>
                        : block_norm_backward_vec_kernel<XT, YT, VPT, false>;
