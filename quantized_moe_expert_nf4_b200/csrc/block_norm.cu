@@ -35,16 +35,15 @@ namespace {
 constexpr int kMaxNormH = 16384;
 
 // Rows of any width, stride and base.
-template <class XT, class YT, int VPT>
-__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 3 : VPT == 2 ? 2 : 1)
+template <class XT, class YT, int VPT, int T>
+__global__ void __launch_bounds__(T, VPT == 1 ? 768 / T : 1)
     block_norm_forward_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
   // Buffers alternate by row: a row may have one sum only, and so no other
   // barrier before the next row's.
   __shared__ float red[2][2][64];
-  const int T = blockDim.x;
-  const Cols<VPT> c{T, static_cast<int>(threadIdx.x), a.H};
-  Rows<XT, YT, VPT, false> rows(a, c, ring);
+  const Cols<VPT, T> c{static_cast<int>(threadIdx.x), a.H};
+  Rows<XT, YT, VPT, T, false> rows(a, c, ring);
   const F2 offset = f2(a.offset);
   int odd = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, odd ^= 1) {
@@ -208,23 +207,34 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT < 4 ? 2 : 1)
   }
 }
 
-template <class XT, class YT, int VPT>
-cudaError_t launch_groups(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  const bool all = a.y.p && a.w_next && a.w_post;
-  auto* kernel = !vec  ? block_norm_forward_kernel<XT, YT, VPT>
-                 : all ? block_norm_forward_vec_kernel<XT, YT, VPT, true>
-                       : block_norm_forward_vec_kernel<XT, YT, VPT, false>;
+template <class K>
+cudaError_t launch_kernel(K kernel, const NormArgs& a, const NormShape& s, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
   kernel<<<s.grid, s.T, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
+template <class XT, class YT, int VPT>
+cudaError_t launch_vec(const NormArgs& a, const NormShape& s, cudaStream_t stream) {
+  const bool all = a.y.p && a.w_next && a.w_post;
+  return all ? launch_kernel(block_norm_forward_vec_kernel<XT, YT, VPT, true>, a, s, stream)
+             : launch_kernel(block_norm_forward_vec_kernel<XT, YT, VPT, false>, a, s, stream);
+}
+
 template <class XT, class YT>
 cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  if (s.vpt == 1) return launch_groups<XT, YT, 1>(a, s, vec, stream);
-  if (s.vpt == 2) return launch_groups<XT, YT, 2>(a, s, vec, stream);
-  return launch_groups<XT, YT, 4>(a, s, vec, stream);
+  if (vec)
+    return s.vpt == 1   ? launch_vec<XT, YT, 1>(a, s, stream)
+           : s.vpt == 2 ? launch_vec<XT, YT, 2>(a, s, stream)
+                        : launch_vec<XT, YT, 4>(a, s, stream);
+  // norm_shape() rounds these rows' threads to one of the sizes below.
+  if (s.vpt == 4) return launch_kernel(block_norm_forward_kernel<XT, YT, 4, 512>, a, s, stream);
+  if (s.vpt == 2) return launch_kernel(block_norm_forward_kernel<XT, YT, 2, 384>, a, s, stream);
+  if (s.T == 64) return launch_kernel(block_norm_forward_kernel<XT, YT, 1, 64>, a, s, stream);
+  if (s.T == 128) return launch_kernel(block_norm_forward_kernel<XT, YT, 1, 128>, a, s, stream);
+  if (s.T == 256) return launch_kernel(block_norm_forward_kernel<XT, YT, 1, 256>, a, s, stream);
+  return launch_kernel(block_norm_forward_kernel<XT, YT, 1, 384>, a, s, stream);
 }
 
 // out[q][col] = sum over parts of partial[q][part][col], in a fixed order: 32
@@ -257,13 +267,13 @@ __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel
 
 constexpr int kSms = 148;
 
-// Threads of a row, their groups, and the persistent CTAs.  The workspace query
-// and the launch agree because both go by M and H alone.
-NormShape norm_shape(int64_t M, int H, int threads_per_sm) {
+// Threads of a row, their groups, and the persistent CTAs.
+NormShape norm_shape(int64_t M, int H, int threads_per_sm, bool vec) {
   const int nvec = (H + 7) / 8;
   NormShape s{};
   s.vpt = nvec <= norm_threads(1) ? 1 : nvec <= 2 * norm_threads(2) ? 2 : 4;
   s.T = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+  if (!vec) s.T = s.vpt == 4 ? 512 : s.vpt == 2 || s.T > 256 ? 384 : s.T > 128 ? 256 : s.T > 64 ? 128 : 64;
   const int per_sm = std::min(16, std::max(1, threads_per_sm / s.T));
   s.grid = static_cast<int>(std::min<int64_t>(M, kSms * per_sm));
   return s;
@@ -275,21 +285,21 @@ struct Moves {
   bool vec, units;
 };
 
-// The ring: as many stages (2 to 4) as leave room for the SM's other CTAs, or, of
-// rows too long for that, none.  Returns whether rows are moved as vectors.
-bool plan_ring(NormArgs* a, const NormShape& s, const Moves& moves, bool x_f32, bool y_f32, int threads_per_sm) {
-  for (RowDst* d : {&a->r, &a->n, &a->dx, &a->dy}) d->step = d->row * s.grid;
+// The shape, and the ring: as many stages (2 to 4) as leave room for the SM's other
+// CTAs, or, of rows too long for that, none.  Returns whether rows are moved as vectors.
+bool plan(NormArgs* a, NormShape* s, const Moves& moves, bool x_f32, bool y_f32, int threads_per_sm) {
   constexpr uint32_t kRoom = 216 * 1024;
-  const int ctas = std::min(16, std::max(1, threads_per_sm / s.T));
-  for (const bool vec : {true, false}) {
-    if (vec ? !moves.vec : !moves.units) continue;
+  bool vec = moves.vec;
+  for (;; vec = false) {
+    *s = norm_shape(a->M, a->H, threads_per_sm, vec);
+    for (RowDst* d : {&a->r, &a->n, &a->dx, &a->dy}) d->step = d->row * s->grid;
     uint32_t off = 0;
     auto place = [&](RowSrc* r, bool f32) {
       if (!r->p) return;
       r->row = r->ld * (f32 ? 4 : 2);
-      r->step = r->row * s.grid;
+      r->step = r->row * s->grid;
       r->off = off;
-      off += vec ? static_cast<uint32_t>(s.T * s.vpt * 8 * (f32 ? 4 : 2))
+      off += vec ? static_cast<uint32_t>(s->T * s->vpt * 8 * (f32 ? 4 : 2))
                  : static_cast<uint32_t>(align_up(static_cast<size_t>(a->H) * (f32 ? 4 : 2), 16) + 16);
     };
     place(&a->dr, x_f32);
@@ -297,9 +307,11 @@ bool plan_ring(NormArgs* a, const NormShape& s, const Moves& moves, bool x_f32, 
     place(&a->dn, a->n_f32);
     place(&a->y, y_f32);
     place(&a->gate, a->gate_f32);
+    const int ctas = std::min(16, std::max(1, threads_per_sm / s->T));
     a->stage_bytes = off;
     a->stages = static_cast<int>(std::max(2u, std::min(4u, kRoom / ctas / off)));
-    if (a->stages * off <= kRoom) return vec;
+    if ((vec || moves.units) && a->stages * off <= kRoom) return vec;
+    if (!vec) break;
   }
   a->stages = 0;
   return false;
@@ -421,9 +433,9 @@ e4b_status e4b_block_norm_forward(const void* x, e4b_dtype x_dtype, int64_t ldx,
   a.r.row = ldr * size_of(x_dtype);
   a.n.p = n;
   a.n.row = ldn * size_of(n_dtype);
-  const NormShape s = norm_shape(M, a.H, kForwardThreads);
+  NormShape s{};
   const bool x_f32 = x_dtype == E4B_F32, y_f32 = y && y_dtype == E4B_F32;
-  const bool vec = plan_ring(&a, s, moves, x_f32, y_f32, kForwardThreads);
+  const bool vec = plan(&a, &s, moves, x_f32, y_f32, kForwardThreads);
   LaunchScope ls("block_norm.forward", st);
   if (cudaError_t err = launch_block_norm_forward(a, x_f32, y_f32, s, vec, st); err != cudaSuccess)
     return cuda_fail(err, "block norm forward launch");
@@ -433,8 +445,10 @@ e4b_status e4b_block_norm_forward(const void* x, e4b_dtype x_dtype, int64_t ldx,
 
 size_t e4b_block_norm_backward_workspace_size(int64_t M, const e4b_block_norm* norm) {
   if (!norm || M < 1 || norm->H < 1 || norm->H > kMaxNormH) return 0;
-  const NormShape s = norm_shape(M, static_cast<int>(norm->H), kBackwardThreads);
-  return static_cast<size_t>(3) * s.grid * norm->H * sizeof(float);
+  // of the two ways to move rows, the one with more CTAs (fewer threads each)
+  const int parts = std::max(norm_shape(M, static_cast<int>(norm->H), kBackwardThreads, true).grid,
+                             norm_shape(M, static_cast<int>(norm->H), kBackwardThreads, false).grid);
+  return static_cast<size_t>(3) * parts * norm->H * sizeof(float);
 }
 
 e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn, e4b_dtype n_dtype, int64_t lddn,
@@ -480,12 +494,12 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
   a.partial = static_cast<float*>(workspace);
   bool vec = false;
   if (M > 0) {
-    const NormShape s = norm_shape(M, a.H, kBackwardThreads);
-    a.parts = s.grid;
+    NormShape s{};
     const bool x_f32 = x_dtype == E4B_F32, y_f32 = y && y_dtype == E4B_F32;
     // the partial sums' rows are vectors of 32 bytes
     moves.vec = moves.vec && vec_base(workspace, E4B_F32);
-    vec = plan_ring(&a, s, moves, x_f32, y_f32, kBackwardThreads);
+    vec = plan(&a, &s, moves, x_f32, y_f32, kBackwardThreads);
+    a.parts = s.grid;
     LaunchScope ls("block_norm.backward", st);
     if (cudaError_t err = launch_block_norm_backward(a, x_f32, y_f32, s, vec, st); err != cudaSuccess)
       return cuda_fail(err, "block norm backward launch");

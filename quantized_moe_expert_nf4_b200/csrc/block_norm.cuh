@@ -237,23 +237,42 @@ struct VecCols {
 // ---- other rows -----------------------------------------------------------------------------
 // Columns j T + t, j < 8 VPT, of thread t, so that a warp's accesses are adjacent; a
 // group v is its columns j = 8 v .. 8 v + 7.  Columns past H read as zero and
-// are not written.
-template <int VPT>
+// are not written.  T is known at compile time: an element then costs its
+// load and little else (the addresses differ by constants).
+template <int VPT, int T>
 struct Cols {
-  int T, t, H;
+  int t, H;
   __device__ __forceinline__ int col(int v, int j) const { return (v * 8 + j) * T + t; }
+  // Whether any thread has columns 2 q and 2 q + 1 of group v (uniform).
+  __device__ __forceinline__ bool any(int v, int q) const { return (v * 8 + 2 * q) * T < H; }
+  template <class E, class At>
+  __device__ __forceinline__ F8 gather(int v, At at) const {
+    F8 f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float x = 0.0f, y = 0.0f;
+      if (any(v, q)) {
+        if (col(v, 2 * q) < H) x = at((v * 8 + 2 * q) * T);
+        if (col(v, 2 * q + 1) < H) y = at((v * 8 + 2 * q + 1) * T);
+      }
+      f.p[q] = f2(x, y);
+    }
+    return f;
+  }
   template <class E>
   __device__ __forceinline__ F8 load(const E* row, int v) const {
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = col(v, j) < H ? load1(row + col(v, j)) : 0.0f;
-    return set8(f);
+    const E* p = row + t;
+    return gather<E>(v, [&](int i) { return load1(p + i); });
   }
   template <class E>
   __device__ __forceinline__ void store(E* row, int v, const F8& f) const {
+    E* p = row + t;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col(v, j) < H) store1(row + col(v, j), get8(f, j));
+    for (int q = 0; q < 4; ++q) {
+      if (!any(v, q)) break;
+      if (col(v, 2 * q) < H) store1(p + (v * 8 + 2 * q) * T, lo(f.p[q]));
+      if (col(v, 2 * q + 1) < H) store1(p + (v * 8 + 2 * q + 1) * T, hi(f.p[q]));
+    }
   }
   // The element type known at run time only (uniform over the launch).
   __device__ __forceinline__ F8 load(const void* row, int f32, int v) const {
@@ -269,36 +288,40 @@ struct Cols {
   // touches.  Its neighbours' ends come along, but nothing past the last row's end.
   template <class E>
   __device__ __forceinline__ void fetch(unsigned char* stage, const RowSrc& s, int64_t m, int64_t M) const {
-    const E* row = static_cast<const E*>(s.p) + m * s.ld;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row), lead = at & 15;
-    const uintptr_t end = at + ((M - 1 - m) * s.ld + H) * sizeof(E);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(s.p) + m * s.row, lead = at & 15;
     const int bytes = static_cast<int>(lead) + H * static_cast<int>(sizeof(E));
-    for (int u = t; u * 16 < bytes; u += T) {
-      const uintptr_t from = at - lead + u * 16;
-      cp16(smem_addr(stage + s.off) + u * 16, reinterpret_cast<const void*>(from),
-           end - from < 16 ? static_cast<int>(end - from) : 16);
+    const uint32_t dst = smem_addr(stage + s.off);
+    const char* src = reinterpret_cast<const char*>(at - lead);
+    // the units of other rows end inside the tensor; the last few rows' may not
+    const bool inside = at - lead + ((bytes + 15) & ~15) <= reinterpret_cast<uintptr_t>(s.p) + (M - 1) * s.row + H * sizeof(E);
+    if (inside) {
+      for (int u = t * 16; u < bytes; u += T * 16) cp16(dst + u, src + u);
+    } else {
+      const int64_t left = static_cast<int64_t>(reinterpret_cast<uintptr_t>(s.p) + (M - 1) * s.row + H * sizeof(E) - (at - lead));
+      for (int u = t * 16; u < bytes; u += T * 16) cp16(dst + u, src + u, left - u < 16 ? static_cast<int>(left - u) : 16);
     }
   }
   // Group v of row m, from the stage that fetch() filled.
   template <class E>
   __device__ __forceinline__ F8 staged(const unsigned char* stage, const RowSrc& s, int64_t m, int v) const {
-    const uintptr_t lead = reinterpret_cast<uintptr_t>(static_cast<const E*>(s.p) + m * s.ld) & 15;
-    return load(reinterpret_cast<const E*>(stage + s.off + lead), v);
+    const uint32_t lead = (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s.p)) + static_cast<uint32_t>(m * s.row)) & 15u;
+    const E* p = reinterpret_cast<const E*>(stage + s.off + lead) + t;
+    return gather<E>(v, [&](int i) { return load1(p + i); });
   }
 };
 
 // The rows of a CTA, one after another, from a ring, or from memory where they are too
 // long for it or their bases are not 16-byte aligned.
-template <class XT, class YT, int VPT, bool BWD>
+template <class XT, class YT, int VPT, int T, bool BWD>
 struct Rows {
   const NormArgs& a;
-  const Cols<VPT>& c;
+  const Cols<VPT, T>& c;
   unsigned char* ring;
   unsigned char* cur;
   int put_stage = 0, stage = 0;
   int64_t put_row;
 
-  __device__ __forceinline__ Rows(const NormArgs& a_, const Cols<VPT>& c_, unsigned char* ring_)
+  __device__ __forceinline__ Rows(const NormArgs& a_, const Cols<VPT, T>& c_, unsigned char* ring_)
       : a(a_), c(c_), ring(ring_), cur(ring_), put_row(blockIdx.x) {
     for (int i = 0; i + 1 < a.stages; ++i) put();
   }

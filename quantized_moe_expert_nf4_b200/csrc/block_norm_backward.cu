@@ -5,16 +5,15 @@ namespace e4b {
 namespace {
 
 // Rows of any width, stride and base.
-template <class XT, class YT, int VPT>
-__global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
+template <class XT, class YT, int VPT, int T>
+__global__ void __launch_bounds__(T, VPT == 1 ? 768 / T : 1)
     block_norm_backward_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
   // Buffers alternate by row: a row may have one sum only, and so no other
   // barrier before the next row's.
   __shared__ float red[2][2][64];
-  const int T = blockDim.x;
-  const Cols<VPT> c{T, static_cast<int>(threadIdx.x), a.H};
-  Rows<XT, YT, VPT, true> rows(a, c, ring);
+  const Cols<VPT, T> c{static_cast<int>(threadIdx.x), a.H};
+  Rows<XT, YT, VPT, T, true> rows(a, c, ring);
   const bool has_y = a.y.p != nullptr, next = a.w_next != nullptr, post = a.w_post != nullptr;
   const int kind = a.gate_kind;
   const F2 offset = f2(a.offset);
@@ -257,23 +256,34 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
   }
 }
 
-template <class XT, class YT, int VPT>
-cudaError_t launch_groups(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  const bool all = a.y.p && a.w_next && a.w_post && a.dr.p && a.dx.p && a.dy.p;
-  auto* kernel = !vec  ? block_norm_backward_kernel<XT, YT, VPT>
-                 : all ? block_norm_backward_vec_kernel<XT, YT, VPT, true>
-                       : block_norm_backward_vec_kernel<XT, YT, VPT, false>;
+template <class K>
+cudaError_t launch_kernel(K kernel, const NormArgs& a, const NormShape& s, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
   kernel<<<s.grid, s.T, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
+template <class XT, class YT, int VPT>
+cudaError_t launch_vec(const NormArgs& a, const NormShape& s, cudaStream_t stream) {
+  const bool all = a.y.p && a.w_next && a.w_post && a.dr.p && a.dx.p && a.dy.p;
+  return all ? launch_kernel(block_norm_backward_vec_kernel<XT, YT, VPT, true>, a, s, stream)
+             : launch_kernel(block_norm_backward_vec_kernel<XT, YT, VPT, false>, a, s, stream);
+}
+
 template <class XT, class YT>
 cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  if (s.vpt == 1) return launch_groups<XT, YT, 1>(a, s, vec, stream);
-  if (s.vpt == 2) return launch_groups<XT, YT, 2>(a, s, vec, stream);
-  return launch_groups<XT, YT, 4>(a, s, vec, stream);
+  if (vec)
+    return s.vpt == 1   ? launch_vec<XT, YT, 1>(a, s, stream)
+           : s.vpt == 2 ? launch_vec<XT, YT, 2>(a, s, stream)
+                        : launch_vec<XT, YT, 4>(a, s, stream);
+  // norm_shape() rounds these rows' threads to one of the sizes below.
+  if (s.vpt == 4) return launch_kernel(block_norm_backward_kernel<XT, YT, 4, 512>, a, s, stream);
+  if (s.vpt == 2) return launch_kernel(block_norm_backward_kernel<XT, YT, 2, 384>, a, s, stream);
+  if (s.T == 64) return launch_kernel(block_norm_backward_kernel<XT, YT, 1, 64>, a, s, stream);
+  if (s.T == 128) return launch_kernel(block_norm_backward_kernel<XT, YT, 1, 128>, a, s, stream);
+  if (s.T == 256) return launch_kernel(block_norm_backward_kernel<XT, YT, 1, 256>, a, s, stream);
+  return launch_kernel(block_norm_backward_kernel<XT, YT, 1, 384>, a, s, stream);
 }
 
 }  // namespace
