@@ -13,7 +13,7 @@
 // activation's derivative and both products with it.
 //
 // Bound: tensor cores from a few hundred rows; below, the weights' bytes.
-// Warps: 0 TMA producer, 1 MMA issuer, 2-5 epilogue.  A persistent CTA (or pair)
+// Warps: 0 TMA producer, 1 MMA issuer, 2-5 (2-9) epilogue.  A persistent CTA (or pair)
 // walks the tiles; two accumulator sets let an epilogue run under the next
 // tile's MMAs.  Tiles: 256 x 256 by a CTA pair (each CTA holds half of A's and B's
 // rows, so a stage is 32 KB for 2 x 128 x 256 x 64 products), or 128 x 128 and
@@ -41,7 +41,6 @@ namespace {
 
 constexpr int kBK = 64;                       // k per stage: one 128-byte swizzle row
 constexpr int kTileM = 128;                   // rows per CTA
-constexpr int kThreads = 6 * 32;
 constexpr int kWarpEpi = 2;
 constexpr uint32_t kABytes = kTileM * 128;
 constexpr uint32_t kPieceBytes = 32 * 64;     // staged output: 32 rows x 32 bf16, 64-byte swizzle
@@ -63,17 +62,20 @@ struct Layout {
   // MN-major rows come in blocks of 64; a last block may be used in part
   static constexpr uint32_t kBBytes = BMN ? (S::kBRows + 63) / 64 * 8192 : S::kBRows * 128;
   static constexpr uint32_t kStage = kABytes + kBBytes;
-  // Output pieces of an epilogue warp: a ring of single ones, or two sets of three, so
-  // that one set is filled while the other's stores read it.
-  static constexpr int kPieces = EPI == kEpiPlain ? 4 : 6;
-  static constexpr uint32_t kStageOutBytes = 4 * kPieces * kPieceBytes;
-  static constexpr uint32_t kStageInBytes = EPI == kEpiDglu ? 4 * 4 * kPieceBytes : 0;  // two pairs of pieces per warp
-  static constexpr int kFit = static_cast<int>((kSmemMax - 2048 - kStageOutBytes - kStageInBytes) / kStage);
+  // The activation's derivative keeps one warp per scheduler busy longer than a
+  // tile's MMAs take (161 us of a kernel whose MMAs take 103): two of them.
+  static constexpr int kEpiWarps = EPI == kEpiDglu ? 8 : 4;
+  static constexpr int kThreads = (kWarpEpi + kEpiWarps) * 32;
+  // Pieces of an epilogue warp.  Plain: a ring of single ones.  Gated: two sets of h,
+  // gate and up, one filled while the other's stores read it.  Derivative: h, and
+  // two pairs of gate and up that are loaded, replaced by their gradients and stored.
+  static constexpr int kPieces = EPI == kEpiPlain ? 4 : EPI == kEpiGlu ? 6 : 5;
+  static constexpr uint32_t kStageOutBytes = kEpiWarps * kPieces * kPieceBytes;
+  static constexpr int kFit = static_cast<int>((kSmemMax - 2048 - kStageOutBytes) / kStage);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr uint32_t kOffOut = kStages * kStage;
-  static constexpr uint32_t kOffIn = kOffOut + kStageOutBytes;
-  static constexpr uint32_t kOffBar = kOffIn + kStageInBytes;
-  static constexpr uint32_t kSmem = kOffBar + (2 * kStages + 4 + 8) * 8 + 16 + 1024;
+  static constexpr uint32_t kOffBar = kOffOut + kStageOutBytes;
+  static constexpr uint32_t kSmem = kOffBar + (2 * kStages + 4 + 16) * 8 + 16 + 1024;
   static_assert(kSmem <= kSmemMax && kStages >= 3, "tile fits");
 };
 
@@ -131,7 +133,7 @@ __device__ __forceinline__ void read_row(const unsigned char* piece, int lane, f
 
 // AMN, BMN: the operand's rows are contiguous in memory (MN-major).
 template <class S, bool AMN, bool BMN, int EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ CUtensorMap tm_o0, const __grid_constant__ CUtensorMap tm_o1,
                     const __grid_constant__ CUtensorMap tm_o2, const __grid_constant__ CUtensorMap tm_i0,
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = empty + KS;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* in_full = acc_empty + 2;  // [epilogue warp][2]: its pre-activations' pieces
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
@@ -159,9 +161,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], 4 * CG);
+      mbar_init(&acc_empty[s], L::kEpiWarps * CG);
     }
-    for (int s = 0; s < 8; ++s) mbar_init(&in_full[s], 1);
+    for (int s = 0; s < 16; ++s) mbar_init(&in_full[s], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -299,7 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // kEpiDglu: the saved gate and up pieces of the next 32 columns are loaded while
     // these are worked on, the first ones of a tile while its MMAs run.
-    unsigned char* in_pieces = smem + L::kOffIn + (warp - kWarpEpi) * 4 * kPieceBytes;
+    // A pair of warps with the same rows takes the columns' halves.
+    constexpr int kCols = kOutCols * 4 / L::kEpiWarps;
+    const int c_first = L::kEpiWarps == 8 ? ((warp - kWarpEpi) >> 2) * kCols : 0;
+    unsigned char* in_pieces = pieces + kPieceBytes;
     uint64_t* in_bar = in_full + (warp - kWarpEpi) * 2;
     uint32_t in_put = 0, in_get = 0;
     auto put_in = [&](int col, int row0) {
@@ -316,7 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row0 = (t % p.m_tiles) * (kTileM * CG) + rank * kTileM + q * 32;
       const int col0 = (t / p.m_tiles) * kOutCols;
       if constexpr (EPI == kEpiDglu)
-        if (row0 < p.rows) put_in(col0, row0);
+        if (row0 < p.rows && col0 + c_first < p.cols) {
+          if (lane == 0) bulk_wait_group_read<0>();
+          put_in(col0 + c_first, row0);
+        }
       if (!mbar_wait(&acc_full[slot], (j >> 1) & 1)) {
         record_error(p.err, kErrWaitFull);
         break;
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + slot * BN;
 #pragma unroll 1
-      for (int c = 0; c < kOutCols; c += 32) {
+      for (int c = c_first; c < c_first + kCols; c += 32) {
         const int col = col0 + c;
         if (row0 >= p.rows || col >= p.cols) break;
         float v[32];
@@ -367,18 +375,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           float g[32], u[32];
-          if (c + 32 < kOutCols && col + 32 < p.cols) put_in(col + 32, row0);
+          unsigned char* in = in_pieces + (in_get & 1) * 2 * kPieceBytes;
+          if (lane == 0) bulk_wait_group_read<0>();  // the last stores, of h and of the other pair
+          if (c + 32 < c_first + kCols && col + 32 < p.cols) put_in(col + 32, row0);
           if (!mbar_wait(&in_bar[in_get & 1], (in_get >> 1) & 1)) {
             record_error(p.err, kErrWaitFull);
             ok = false;
+            tmem_ld_wait();
             break;
           }
-          read_row(in_pieces + (in_get & 1) * 2 * kPieceBytes, lane, g);
-          read_row(in_pieces + (in_get & 1) * 2 * kPieceBytes + kPieceBytes, lane, u);
+          read_row(in, lane, g);
+          read_row(in + kPieceBytes, lane, u);
           ++in_get;
           tmem_ld_wait();
-          unsigned char* set = pieces + (piece_no++ & 1) * 3 * kPieceBytes;
-          if (lane == 0) bulk_wait_group_read<1>();  // the stores that last read this set
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -389,15 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             g[i] = dh * u[i] * da;   // gate's gradient
             u[i] = dh * a;           // up's gradient
           }
-          stage_row(set, lane, v);
-          stage_row(set + kPieceBytes, lane, g);
-          stage_row(set + 2 * kPieceBytes, lane, u);
+          stage_row(pieces, lane, v);
+          stage_row(in, lane, g);
+          stage_row(in + kPieceBytes, lane, u);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tm_o0, set, col, row0);
-            tma_store_2d(&tm_o1, set + kPieceBytes, col, row0);
-            tma_store_2d(&tm_o2, set + 2 * kPieceBytes, col, row0);
+            tma_store_2d(&tm_o0, pieces, col, row0);
+            tma_store_2d(&tm_o1, in, col, row0);
+            tma_store_2d(&tm_o2, in + kPieceBytes, col, row0);
             bulk_commit_group();
           }
         }
@@ -481,7 +490,7 @@ cudaError_t launch_shape(const Gemm& g, int sm_count, cudaStream_t stream) {
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sm_count / S::CG) * S::CG));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
