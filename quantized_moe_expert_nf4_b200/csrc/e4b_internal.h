@@ -266,6 +266,7 @@ struct GemvArgs {
   void* out;          // [M, ldo]
   bool out_f32;
   int64_t ldo;
+  bool after_input;   // x is written by the launch before this one: the weights' first pieces are loaded meanwhile
 };
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream);
 

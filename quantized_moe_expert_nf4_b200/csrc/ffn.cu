@@ -48,6 +48,16 @@ constexpr uint32_t kSmemMax = 227 * 1024;
 
 enum Epi { kEpiPlain = 0, kEpiGlu = 1, kEpiDglu = 2 };
 
+// The products of one call are launched so that one may start before the last has
+// ended (programmatic dependent launch).  kAfterAll: an ordinary launch.
+// kAfterInput: it reads what the launch before it writes, and waits for it
+// before its first load; its start-up is hidden.  kAfterNothing: it reads what an
+// earlier one wrote, which had ended when the launch before it allowed this one to
+// start (each allows it only after its own wait), so its tiles fill the SMs that
+// run out of work in the launch before; it waits for that one's end before its own,
+// so that the stream's order holds for what follows.
+enum After { kAfterAll = 0, kAfterInput = 1, kAfterNothing = 2 };
+
 // CTAs of a tile (1, or a pair) and its columns; where everything lies in shared
 // memory, for an operand B that is MN-major or not and an epilogue.
 template <int CG_, int BN_>
@@ -85,6 +95,7 @@ struct TileParams {
   int half;                // gated: first up row of B (I)
   int act;
   int write_pre;           // kEpiGlu: also store the pre-activations
+  int after;               // how the kernel follows the launch before it (After)
   int* err;
 };
 
@@ -183,6 +194,8 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (p.after == kAfterInput) pdl_wait();
+  pdl_launch_dependents();
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     // The stage's bytes of both CTAs of a pair are counted on rank 0's barrier.
@@ -424,6 +437,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
       for (; in_get < in_put; ++in_get) mbar_wait(&in_bar[in_get & 1], (in_get >> 1) & 1);
     if (lane == 0) bulk_wait_group_all();
   }
+  if (p.after == kAfterNothing) pdl_wait();
   tc_fence_before();
   if constexpr (CG == 2)
     cluster_sync_all();  // the pair's barriers and tiles are used from both sides
@@ -493,12 +507,14 @@ cudaError_t launch_shape(const Gemm& g, int sm_count, cudaStream_t stream) {
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S::CG;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = S::CG > 1 ? 1 : 0;
+  cfg.numAttrs = p.after == kAfterAll ? 1 : 2;
   LaunchScope ls(g.name, stream);
   return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<S, AMN, BMN, EPI>, ta, tb, to[0], to[1], to[2], ti[0], ti[1], p);
 }
@@ -586,6 +602,7 @@ e4b_status e4b_gated_ffn_forward(const uint16_t* x, int64_t M, int64_t ldx, cons
     a.out = h;
     a.ldo = I;
     if (cudaError_t err = launch_gemv(a, st); err != cudaSuccess) return cuda_fail(err, "ffn gate_up launch");
+    a.after_input = true;
     a.x = h;
     a.ldx = I;
     a.w = w->down;
@@ -628,6 +645,7 @@ e4b_status e4b_gated_ffn_forward(const uint16_t* x, int64_t M, int64_t ldx, cons
   d.p.cols = H;
   d.p.K = I;
   d.p.err = g.p.err;
+  d.p.after = kAfterInput;
   if (cudaError_t err = launch_gemm<false, false, kEpiPlain>(d, di.sm_count, st); err != cudaSuccess)
     return cuda_fail(err, "ffn down launch");
   set_path("ffn.forward.tc");
@@ -678,9 +696,13 @@ e4b_status e4b_gated_ffn_backward(const uint16_t* x, int64_t M, int64_t ldx, con
   g.p.err = static_cast<int*>(workspace);
   if (cudaError_t err = launch_gemm<false, true, kEpiDglu>(g, di.sm_count, st); err != cudaSuccess)
     return cuda_fail(err, "ffn dh launch");
+  // The gradients read what dh writes; the first of them waits for it, the others start behind that one.
+  int after = kAfterInput;
   if (dx) {
     Gemm d{};
     d.name = "ffn.dx";
+    d.p.after = after;
+    after = kAfterNothing;
     d.a = {dpre, M, 2 * w->I, 2 * w->I};
     d.b = {w->gate_up, 2 * w->I, w->H, w->H};
     d.out[0] = {dx, M, w->H, w->H};
@@ -694,6 +716,8 @@ e4b_status e4b_gated_ffn_backward(const uint16_t* x, int64_t M, int64_t ldx, con
   if (dgate_up) {
     Gemm d{};
     d.name = "ffn.dgate_up";
+    d.p.after = after;
+    after = kAfterNothing;
     d.a = {dpre, M, 2 * w->I, 2 * w->I};
     d.b = {x, M, w->H, ldx};
     d.out[0] = {dgate_up, 2 * w->I, w->H, w->H};
@@ -707,6 +731,7 @@ e4b_status e4b_gated_ffn_backward(const uint16_t* x, int64_t M, int64_t ldx, con
   if (ddown) {
     Gemm d{};
     d.name = "ffn.ddown";
+    d.p.after = after;
     d.a = {dout, M, w->H, w->H};
     d.b = {h, M, w->I, w->I};
     d.out[0] = {ddown, w->H, w->I, w->I};

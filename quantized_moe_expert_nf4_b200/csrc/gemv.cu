@@ -29,6 +29,7 @@
 
 #include <algorithm>
 
+#include "async.cuh"
 #include "common.cuh"
 #include "e4b_internal.h"
 
@@ -278,6 +279,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
       }
     }
   };
+  if (a.after_input) pdl_wait();
+  pdl_launch_dependents();
   if (first < p.chunks) load_x(first);
 
   const unsigned char* lane_table = smem + lane * 4;
@@ -445,12 +448,14 @@ cudaError_t launch_one(const Params& p, int grid, cudaStream_t stream) {
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = p.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  cfg.numAttrs = p.a.after_input ? 2 : 1;
   LaunchScope ls(FMT == kFmtBf16 ? "gemv.bf16" : FMT == kFmtInt4 ? "gemv.int4" : "gemv.codebook", stream);
   return cudaLaunchKernelEx(&cfg, gemv_kernel<FMT, GB, NT, RT, TWO>, p);
 }
