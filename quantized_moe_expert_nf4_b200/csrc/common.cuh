@@ -56,7 +56,7 @@ __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + __expf(-
 
 // GELU in its tanh form: z/2 (1 + tanh(u)) = z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3).
 __device__ __forceinline__ float gelu_tanh_f32(float z) {
-  return z / (1.0f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+  return __fdividef(z, 1.0f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
 }
 
 template <typename T>

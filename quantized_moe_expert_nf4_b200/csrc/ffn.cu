@@ -60,12 +60,13 @@ enum After { kAfterAll = 0, kAfterInput = 1, kAfterNothing = 2 };
 
 // CTAs of a tile (1, or a pair) and its columns; where everything lies in shared
 // memory, for an operand B that is MN-major or not and an epilogue.
-template <int CG_, int BN_>
+// SPLIT: CTAs of a cluster that share a tile's k blocks.
+template <int CG_, int BN_, int SPLIT_ = 1>
 struct Shape {
-  static constexpr int CG = CG_, BN = BN_;
+  static constexpr int CG = CG_, BN = BN_, SPLIT = SPLIT_;
   static constexpr int kBRows = BN / CG;      // B rows per CTA
   static constexpr uint32_t kCols = BN <= 64 ? 128 : BN <= 128 ? 256 : 512;  // TMEM columns: two accumulator sets
-  static_assert(2 * BN <= 512 && BN % 32 == 0, "tile shape");
+  static_assert(2 * BN <= 512 && BN % 32 == 0 && (SPLIT == 1 || CG == 1), "tile shape");
 };
 template <class S, bool BMN, int EPI>
 struct Layout {
@@ -81,10 +82,13 @@ struct Layout {
   // two pairs of gate and up that are loaded, replaced by their gradients and stored.
   static constexpr int kPieces = EPI == kEpiPlain ? 4 : EPI == kEpiGlu ? 6 : 5;
   static constexpr uint32_t kStageOutBytes = kEpiWarps * kPieces * kPieceBytes;
-  static constexpr int kFit = static_cast<int>((kSmemMax - 2048 - kStageOutBytes) / kStage);
+  // Partial sums of the other CTAs for this one's rows (32 rows x BN fp32 per quarter).
+  static constexpr uint32_t kRecvBytes = S::SPLIT > 1 ? (S::SPLIT - 1) * (4 / S::SPLIT) * S::BN * 128 : 0;
+  static constexpr int kFit = static_cast<int>((kSmemMax - 2048 - kStageOutBytes - kRecvBytes) / kStage);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr uint32_t kOffOut = kStages * kStage;
-  static constexpr uint32_t kOffBar = kOffOut + kStageOutBytes;
+  static constexpr uint32_t kOffRecv = kOffOut + kStageOutBytes;
+  static constexpr uint32_t kOffBar = kOffRecv + kRecvBytes;
   static constexpr uint32_t kSmem = kOffBar + (2 * kStages + 4 + 16) * 8 + 16 + 1024;
   static_assert(kSmem <= kSmemMax && kStages >= 3, "tile fits");
 };
@@ -92,6 +96,7 @@ struct Layout {
 struct TileParams {
   int rows, cols, K;       // of D and the contraction; for the gated tile, cols of h
   int m_tiles, n_tiles;
+  int group;               // row tiles that are walked together (tile_at)
   int half;                // gated: first up row of B (I)
   int act;
   int write_pre;           // kEpiGlu: also store the pre-activations
@@ -142,6 +147,16 @@ __device__ __forceinline__ void read_row(const unsigned char* piece, int lane, f
   }
 }
 
+// Tile t of the walk: `group` row tiles by all column tiles, rows fastest, then the
+// next row tiles.  The tiles at work at one time then form a block whose operands
+// stay in L2.
+__device__ __forceinline__ void tile_at(const TileParams& p, int t, int* m, int* n) {
+  const int per = p.group * p.n_tiles, g = t / per, r = t - g * per;
+  const int rows = min(p.group, p.m_tiles - g * p.group);
+  *n = r / rows;
+  *m = g * p.group + r - *n * rows;
+}
+
 // AMN, BMN: the operand's rows are contiguous in memory (MN-major).
 template <class S, bool AMN, bool BMN, int EPI>
 __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
@@ -161,9 +176,13 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
   uint64_t* in_full = acc_empty + 2;  // [epilogue warp][2]: its pre-activations' pieces
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int SPLIT = S::SPLIT;
   const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
-  const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+  const int part = SPLIT > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / (CG * SPLIT), step = static_cast<int>(gridDim.x) / (CG * SPLIT);
   const int tiles = p.m_tiles * p.n_tiles, KB = (p.K + kBK - 1) / kBK;
+  // This CTA's k blocks: all of them, or its part (never empty, see launch_gemm).
+  const int kb_per = (KB + SPLIT - 1) / SPLIT, kb_first = part * kb_per, kb_end = min(KB, kb_first + kb_per);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
@@ -187,8 +206,8 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
     }
   }
   tc_fence_before();
-  if constexpr (CG == 2)
-    cluster_sync_all();
+  if constexpr (CG == 2 || SPLIT > 1)
+    cluster_sync_all();  // the others have started and set up what this CTA writes to
   else
     __syncthreads();
   tc_fence_after();
@@ -202,8 +221,10 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
-      const int m0 = (t % p.m_tiles) * (kTileM * CG) + rank * kTileM, n_tile = t / p.m_tiles;
-      for (int kb = 0; kb < KB; ++kb, ++it) {
+      int m_tile, n_tile;
+      tile_at(p, t, &m_tile, &n_tile);
+      const int m0 = m_tile * (kTileM * CG) + rank * kTileM;
+      for (int kb = kb_first; kb < kb_end; ++kb, ++it) {
         const int s = it % KS;
         if (it >= KS && !mbar_wait(&empty[s], ((it / KS) - 1) & 1)) {
           record_error(p.err, kErrWaitEmpty);
@@ -256,6 +277,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
       if (ok) ok = mbar_wait(&empty[j % KS], (j / KS) & 1);
       if (!ok && rank == 0) mbar_wait(&full[j % KS], (j / KS) & 1);
     }
+    if constexpr (SPLIT > 1) cluster_sync_all();  // with the epilogue's
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
     if (rank == 0) {
@@ -270,7 +292,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + slot * BN;
-        for (int kb = 0; kb < KB; ++kb, ++it) {
+        for (int kb = kb_first; kb < kb_end; ++kb, ++it) {
           const int s = it % KS;
           if (!mbar_wait(&full[s], (it / KS) & 1)) {
             record_error(p.err, kErrWaitFull);
@@ -285,9 +307,9 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
               const uint64_t ad = AMN ? smem_desc_mn_sw128(a + kk * 2048, 8192) : smem_desc_sw128(a + kk * 32);
               const uint64_t bd = BMN ? smem_desc_mn_sw128(b + kk * 2048, 8192) : smem_desc_sw128(b + kk * 32);
               if constexpr (CG == 2)
-                umma_bf16_pair(d, ad, bd, idesc, (kb | kk) ? 1u : 0u);
+                umma_bf16_pair(d, ad, bd, idesc, kb > kb_first || kk ? 1u : 0u);
               else
-                umma_bf16(d, ad, bd, idesc, (kb | kk) ? 1u : 0u);
+                umma_bf16(d, ad, bd, idesc, kb > kb_first || kk ? 1u : 0u);
             }
             if constexpr (CG == 2)
               umma_commit_pair(&empty[s]);
@@ -306,6 +328,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
         __syncwarp();
       }
     }
+    if constexpr (SPLIT > 1) cluster_sync_all();
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31 = the tile's rows
@@ -331,19 +354,55 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
     };
     for (int t = first; t < tiles && ok; t += step, ++j) {
       const uint32_t slot = j & 1;
-      const int row0 = (t % p.m_tiles) * (kTileM * CG) + rank * kTileM + q * 32;
-      const int col0 = (t / p.m_tiles) * kOutCols;
+      int m_tile, n_tile;
+      tile_at(p, t, &m_tile, &n_tile);
+      const int row0 = m_tile * (kTileM * CG) + rank * kTileM + q * 32;
+      const int col0 = n_tile * kOutCols;
       if constexpr (EPI == kEpiDglu)
-        if (row0 < p.rows && col0 + c_first < p.cols) {
+        if (row0 < p.rows && col0 + c_first < p.cols && q * SPLIT / 4 == part) {
           if (lane == 0) bulk_wait_group_read<0>();
           put_in(col0 + c_first, row0);
         }
       if (!mbar_wait(&acc_full[slot], (j >> 1) & 1)) {
         record_error(p.err, kErrWaitFull);
-        break;
+        ok = false;
+        if constexpr (SPLIT == 1) break;
       }
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + slot * BN;
+      // A split tile: part i of the cluster finishes the rows of quarters [4 i / SPLIT,
+      // 4 (i + 1) / SPLIT); the others leave their sums of those rows in its shared memory.
+      constexpr int kQuarters = 4 / SPLIT;
+      if constexpr (SPLIT > 1) {
+        const int owner = q / kQuarters;
+        if (owner != part && ok) {
+          const int from = part < owner ? part : part - 1;
+          const uint32_t to = cluster_addr(smem + L::kOffRecv + (from * kQuarters + q % kQuarters) * BN * 128 + lane * 4, owner);
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            // of a pair of warps with the same rows, each sends half
+            if (L::kEpiWarps == 8 && (c >= BN / 2) != (warp - kWarpEpi >= 4)) continue;
+            float v[32];
+            tmem_ld_32x32b_x32(acc + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) st_cluster_f32(to + (c + i) * 128, v[i]);
+          }
+        }
+        cluster_sync_all();
+        if (owner != part || !ok) break;
+      }
+      // Columns [at, at + 32) of the tile, of this lane's row.
+      auto add_parts = [&](int at, float v[32]) {
+        if constexpr (SPLIT > 1) {
+#pragma unroll
+          for (int f = 0; f < SPLIT - 1; ++f) {
+            const float* src = reinterpret_cast<const float*>(smem + L::kOffRecv + (f * kQuarters + q % kQuarters) * BN * 128) + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += src[(at + i) * 32];
+          }
+        }
+      };
 #pragma unroll 1
       for (int c = c_first; c < c_first + kCols; c += 32) {
         const int col = col0 + c;
@@ -353,6 +412,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
         if constexpr (EPI == kEpiPlain) {
           unsigned char* piece = pieces + (piece_no++ % L::kPieces) * kPieceBytes;
           tmem_ld_wait();
+          add_parts(c, v);
           if (lane == 0) bulk_wait_group_read<L::kPieces - 1>();  // the store that last read this piece
           __syncwarp();
           stage_row(piece, lane, v);
@@ -366,6 +426,8 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
           float u[32];
           tmem_ld_32x32b_x32(acc + BN / 2 + c, u);
           tmem_ld_wait();
+          add_parts(c, v);
+          add_parts(BN / 2 + c, u);
           unsigned char* set = pieces + (piece_no++ & 1) * 3 * kPieceBytes;
           if (lane == 0) bulk_wait_group_read<1>();  // the stores that last read this set
           __syncwarp();
@@ -401,6 +463,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
           read_row(in + kPieceBytes, lane, u);
           ++in_get;
           tmem_ld_wait();
+          add_parts(c, v);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -501,15 +564,17 @@ cudaError_t launch_shape(const Gemm& g, int sm_count, cudaStream_t stream) {
   p.m_tiles = (p.rows + kTileM * S::CG - 1) / (kTileM * S::CG);
   const int cols = EPI == kEpiGlu ? S::BN / 2 : S::BN;
   p.n_tiles = (p.cols + cols - 1) / cols;
+  p.group = 8;  // 4 to 8 measured best: M=8192 H=I=2880 training step 1085 us against 1140 with all rows
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, sm_count / S::CG) * S::CG));
+  const int64_t ctas = S::CG * S::SPLIT;  // of a cluster
+  cfg.gridDim = dim3(static_cast<unsigned>((S::SPLIT > 1 ? tiles : std::min<int64_t>(tiles, sm_count / S::CG)) * ctas));
   cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S::CG;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -531,6 +596,11 @@ cudaError_t launch_gemm(const Gemm& g, int sm_count, cudaStream_t stream) {
   // 256 x 256 already, and grow with every column taken away.)
   if (tiles(256, 256) >= sm_count / 2) return launch_shape<Shape<2, 256>, AMN, BMN, EPI>(g, sm_count, stream);
   if (tiles(128, 128) >= sm_count) return launch_shape<Shape<1, 128>, AMN, BMN, EPI>(g, sm_count, stream);
+  // Small tiles; where even those are few, two or four CTAs share the k blocks of one.
+  const int64_t small = tiles(128, 64);
+  const int KB = (g.p.K + kBK - 1) / kBK;
+  if (small * 4 <= sm_count && KB >= 16) return launch_shape<Shape<1, 64, 4>, AMN, BMN, EPI>(g, sm_count, stream);
+  if (small * 2 <= sm_count && KB >= 8) return launch_shape<Shape<1, 64, 2>, AMN, BMN, EPI>(g, sm_count, stream);
   return launch_shape<Shape<1, 64>, AMN, BMN, EPI>(g, sm_count, stream);
 }
 
