@@ -1,0 +1,157 @@
+"""The calls around the experts run together, as a decoder block runs them, against the float64 oracles.
+
+    n = N(x; w1);  y = experts(n) + shared(n);  r = x + s * sigmoid(g) * N(y; w2);  n' = N(r; w3)
+
+Serving holds the shared expert and the router in 4 bits and runs a few tokens; training runs the
+shared expert in bf16 and goes back through everything.  Tolerance: that of the routed layer
+(relative Frobenius 1e-2, max-abs 2e-2 of the largest), whose roundings dominate.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import backward, block_norm as bn, ffn, gemv, moe, nf4, routing
+from quantized_moe_expert_nf4_b200 import e4b, synthetic, workloads
+from gpu_util import assert_close_layer, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _setup(M, seed=0):
+    cfg = workloads.small_config("block", E=8, H=256, I=128, k=2)
+    layer = synthetic.make_device_layer(cfg)
+    gp, ga = nf4.quantize_stack(workloads.gate_up_stack(cfg))
+    dp, da = nf4.quantize_stack(workloads.down_stack(cfg))
+    stack = moe.ExpertStack(gp, ga, dp, da, cfg.E, cfg.H, cfg.I, None, None, 0.0)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    t = {"x": rand(M, cfg.H).to(BF), "gate": rand(M, 1).to(BF)}
+    for k in ("w1", "w2", "w3"):
+        t[k] = (1 + 0.1 * rand(cfg.H)).to(BF)
+    t["gate_up"], t["down"] = (0.05 * rand(2 * 192, cfg.H)).to(BF), (0.05 * rand(cfg.H, 192)).to(BF)
+    return cfg, layer, stack, t, rand
+
+
+def _int4(w, group):
+    """Symmetric int4 codes of a matrix in groups, as a checkpoint would hold them."""
+    N, K = w.shape
+    v = w.float().view(N, K // group, group)
+    scale = (v.abs().amax(-1, keepdim=True) / 7).to(BF)
+    q = (torch.round(v / scale.float()) + 8).clamp(0, 15).to(torch.uint8).view(N, K)
+    packed = (q[:, 0::2] * 16 + q[:, 1::2]).contiguous()
+    scale = scale.view(N, K // group).contiguous()
+    return (e4b.GroupWeight(packed, scale, N, K, group, e4b.E4B_QUANT_INT4),
+            gemv.dequantise(packed.cpu().numpy(), _np(scale), group, "int4"))
+
+
+def _empty(*shape, dtype=BF):
+    return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("M", [1, 7])
+def test_serving(M):
+    require_gpu()
+    cfg, layer, stack, t, rand = _setup(M)
+    router, router_w = _int4(0.3 * rand(cfg.E, cfg.H), 32)
+    shared_up, shared_up_w = _int4(t["gate_up"], 64)
+    shared_dn, shared_dn_w = _int4(t["down"], 32)
+    first = e4b.BlockNorm(cfg.H, None, t["w1"], 1e-6)
+    second = e4b.BlockNorm(cfg.H, t["w2"], t["w3"], 1e-6, 0.5, gate_sigmoid=True)
+    n, logits, routed, h, shared = (_empty(M, cfg.H), _empty(M, cfg.E, dtype=F32), _empty(M, cfg.H), _empty(M, 192),
+                                    _empty(M, cfg.H))
+    r, n2 = _empty(M, cfg.H), _empty(M, cfg.H)
+    ws = e4b.workspace(e4b.e4b_moe_expert_forward_workspace_size(M, layer.stack, cfg.k))
+
+    def step():
+        e4b.e4b_block_norm_forward(t["x"], None, None, first, None, n)
+        e4b.e4b_gemv_4bit(n, router, logits)
+        e4b.e4b_moe_expert_forward(n, logits, cfg.k, True, layer.stack, routed, ws)
+        e4b.e4b_gemv_4bit(n, shared_up, h, e4b.E4B_EPI_SWIGLU)
+        e4b.e4b_gemv_4bit(h, shared_dn, shared)
+        e4b.e4b_block_norm_forward(t["x"], routed + shared, t["gate"], second, r, n2)
+
+    step()
+    eager = r.clone(), n2.clone()
+    x = _np(t["x"])
+    rn = bn.forward(x, None, None, bn.Norm(None, _np(t["w1"])))[1]
+    assert_close_layer(_np(logits), rn @ router_w.T, "router logits")
+    ids, w, *_ = routing.route_permute(logits.cpu().numpy(), cfg.k)
+    y = moe.moe_forward_per_token(rn, ids, w, stack)
+    y = y + gemv.product(gemv.product(rn, shared_up_w, True), shared_dn_w)
+    want = bn.forward(x, y, _np(t["gate"]), bn.Norm(_np(t["w2"]), _np(t["w3"]), scale=0.5, sigmoid=True))
+    assert_close_layer(_np(r), want[0], "r")
+    assert_close_layer(_np(n2), want[1], "n")
+    # the whole block captured once and replayed
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    r.fill_(7), n2.fill_(7)
+    graph.replay()
+    assert torch.equal(r, eager[0]) and torch.equal(n2, eager[1])
+    assert e4b.workspace_error(ws) == e4b.E4B_KERNEL_ERR_NONE
+
+
+def test_training():
+    require_gpu()
+    M = 200
+    cfg, layer, stack, t, rand = _setup(M, seed=3)
+    logits = rand(M, cfg.E)
+    dr, dn2 = rand(M, cfg.H).to(BF), rand(M, cfg.H).to(BF)
+    first = e4b.BlockNorm(cfg.H, None, t["w1"], 1e-6)
+    second = e4b.BlockNorm(cfg.H, t["w2"], t["w3"], 1e-6, 0.5, gate_sigmoid=True)
+    shared = e4b.GatedFFN(t["gate_up"], t["down"])
+    n, routed, dense, pre = _empty(M, cfg.H), _empty(M, cfg.H), _empty(M, cfg.H), _empty(M, 384)
+    r, n2 = _empty(M, cfg.H), _empty(M, cfg.H)
+    moe_ws = e4b.workspace(max(e4b.e4b_moe_expert_forward_workspace_size(M, layer.stack, cfg.k),
+                               e4b.e4b_moe_expert_backward_workspace_size(M, layer.stack, cfg.k)))
+    ffn_ws = e4b.workspace(max(e4b.e4b_gated_ffn_forward_workspace_size(M, shared),
+                               e4b.e4b_gated_ffn_backward_workspace_size(M, shared)))
+    norm_ws = e4b.workspace(max(e4b.e4b_block_norm_backward_workspace_size(M, p) for p in (first, second)))
+
+    e4b.e4b_block_norm_forward(t["x"], None, None, first, None, n)
+    e4b.e4b_moe_expert_forward(n, logits, cfg.k, True, layer.stack, routed, moe_ws)
+    e4b.e4b_gated_ffn_forward(n, shared, dense, pre, ffn_ws)
+    y = routed + dense
+    e4b.e4b_block_norm_forward(t["x"], y, t["gate"], second, r, n2)
+
+    got = {k: _empty(cfg.H, dtype=F32) for k in ("w1", "w2", "w3")}
+    got |= {"gate": _empty(M, 1), "gate_up": _empty(384, cfg.H), "down": _empty(cfg.H, 192), "x": _empty(M, cfg.H),
+            "logits": _empty(M, cfg.E, dtype=F32)}
+    d_res, dy, dn_dense, dn_routed = _empty(M, cfg.H), _empty(M, cfg.H), _empty(M, cfg.H), _empty(M, cfg.H, dtype=F32)
+    e4b.e4b_block_norm_backward(dr, dn2, r, y, t["gate"], second, d_res, dy, got["gate"], got["w2"], got["w3"], norm_ws)
+    e4b.e4b_moe_expert_backward(n, logits, cfg.k, True, layer.stack, dy, dn_routed, got["logits"], None, None, moe_ws)
+    e4b.e4b_gated_ffn_backward(n, shared, pre, dy, dn_dense, got["gate_up"], got["down"], ffn_ws)
+    # the two branches' gradients meet in fp32; the residual's is the norm's dr
+    e4b.e4b_block_norm_backward(d_res, dn_routed + dn_dense, t["x"], None, None, first, got["x"], None, None, None,
+                                got["w1"], norm_ws)
+    assert e4b.workspace_error(moe_ws) == 0 and e4b.workspace_error(ffn_ws) == 0
+
+    x, gate = _np(t["x"]), _np(t["gate"])
+    p1, p2 = bn.Norm(None, _np(t["w1"])), bn.Norm(_np(t["w2"]), _np(t["w3"]), scale=0.5, sigmoid=True)
+    lg = logits.cpu().numpy()
+    ids, w, *_ = routing.route_permute(lg, cfg.k)
+    rn = bn.forward(x, None, None, p1)[1]
+    out, rpre, _ = ffn.forward(rn, _np(t["gate_up"]), _np(t["down"]))
+    ry = moe.moe_forward_per_token(rn, ids, w, stack) + out
+    rr, rn2 = bn.forward(x, ry, gate, p2)
+    assert_close_layer(_np(r), rr, "r")
+    assert_close_layer(_np(n2), rn2, "n")
+    b2 = bn.backward(_np(dr), _np(dn2), rr, ry, gate, p2)
+    mdx, mdl, *_ = backward.layer_backward(rn, lg.astype(np.float64), routing.topk(lg, cfg.k), stack, b2["dy"], True)
+    f = ffn.backward(rn, rpre, _np(t["gate_up"]), _np(t["down"]), b2["dy"])
+    b1 = bn.backward(b2["dx"], mdx + f["dx"], x, None, None, p1)
+    want = {"w1": b1["dw_next"], "x": b1["dx"], "w2": b2["dw_post"], "w3": b2["dw_next"], "gate": b2["dgate"], "logits": mdl,
+            "gate_up": f["dgate_up"], "down": f["ddown"]}
+    for k, v in want.items():
+        assert_close_layer(_np(got[k]), v, "gradient of " + k)
