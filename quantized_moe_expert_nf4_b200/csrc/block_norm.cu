@@ -94,39 +94,41 @@ __global__ void __launch_bounds__(T, VPT == 1 ? 768 / T : 1)
   }
 }
 
-// Rows moved as vectors.  ALL: y and both weights are there, the step between two
+// Rows moved as vectors, aligned or shifted (COLS).  ALL: y and both weights are there, the step between two
 // blocks.
-template <class XT, class YT, int VPT, bool ALL>
+template <class XT, class YT, int VPT, class COLS, bool ALL>
 __global__ void __launch_bounds__(norm_threads(VPT), VPT < 4 ? 2 : 1)
     block_norm_forward_vec_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float red[2][2][64];  // as above
   const int T = blockDim.x;
-  const VecCols<VPT> c(T, threadIdx.x, a.H);
+  const COLS c(T, threadIdx.x, a.H);
   const bool has_y = ALL || a.y.p, next = ALL || a.w_next, post = ALL || a.w_post;
   const int kind = a.gate_kind, stages = a.stages;
   const int step = static_cast<int>(gridDim.x);
   auto row_of = [&](const RowSrc& t) { return static_cast<const unsigned char*>(t.p) + blockIdx.x * t.row; };
   const unsigned char *x_p = row_of(a.x), *y_p = row_of(a.y), *g_p = row_of(a.gate);
-  const uint32_t ring_u = smem_addr(ring) + threadIdx.x * 16;
-  const unsigned char* ring_p = ring + threadIdx.x * 16;
+  const uint32_t ring_u = smem_addr(ring) + c.place();
+  const unsigned char* ring_p = ring + c.place();
   int64_t put_row = blockIdx.x;
   int put_stage = 0, stage = 0;
-  // A thread reads its own places only, so that filling the last row's stage needs no barrier.
+  // Aligned: a thread reads its own places only, so that filling the last row's stage
+  // needs no barrier.  Shifted: see below.
   auto put = [&]() {
     if (put_row < a.M) {
+      const int64_t last = a.M - 1 - put_row;
       const uint32_t to = ring_u + put_stage * a.stage_bytes;
-      c.template fetch<XT>(to + a.x.off, x_p);
+      c.template fetch<XT>(to + a.x.off, x_p, a.x, last);
       x_p += a.x.step;
       if (has_y) {
-        c.template fetch<YT>(to + a.y.off, y_p);
+        c.template fetch<YT>(to + a.y.off, y_p, a.y, last);
         y_p += a.y.step;
       }
       if (kind == E4B_GATE_FULL) {
         if (a.gate_f32)
-          c.template fetch<float>(to + a.gate.off, g_p);
+          c.template fetch<float>(to + a.gate.off, g_p, a.gate, last);
         else
-          c.template fetch<uint16_t>(to + a.gate.off, g_p);
+          c.template fetch<uint16_t>(to + a.gate.off, g_p, a.gate, last);
         g_p += a.gate.step;
       }
       put_row += step;
@@ -148,22 +150,43 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT < 4 ? 2 : 1)
   auto w_next = [&](int v) { return kHold ? hold_next : c.vector(a.w_next, a.w_f32, v) + offset; };
   unsigned char* r_p = static_cast<unsigned char*>(a.r.p) + blockIdx.x * a.r.row;
   unsigned char* n_p = static_cast<unsigned char*>(a.n.p) + blockIdx.x * a.n.row;
+  auto flush = [&](int set, unsigned char* r_row, unsigned char* n_row) {
+    if constexpr (COLS::kShared) {
+      const unsigned char* out = ring + a.out_off + set * a.out_bytes;
+      if (has_y) c.template flush<XT>(r_row, out + a.out_slot[0]);
+      if (next) {
+        if (a.n_f32)
+          c.template flush<float>(n_row, out + a.out_slot[1]);
+        else
+          c.template flush<uint16_t>(n_row, out + a.out_slot[1]);
+      }
+    }
+  };
   int odd = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, r_p += a.r.step, n_p += a.n.step) {
     cp_wait(stages);
+    unsigned char *r_s = nullptr, *n_s = nullptr;
+    if constexpr (COLS::kShared) {
+      // The copies are in and the last row is done with: its stage and its outputs' rows.
+      // Two sets of output rows: one is written while the other is put together.
+      __syncthreads();
+      unsigned char* out = ring + a.out_off + odd * a.out_bytes;
+      r_s = out + a.out_slot[0], n_s = out + a.out_slot[1];
+      if (m != blockIdx.x) flush(odd ^ 1, r_p - a.r.step, n_p - a.n.step);
+    }
     put();
     const unsigned char* cur = ring_p + stage * a.stage_bytes;
     stage = stage + 1 == stages ? 0 : stage + 1;
     F8 r[VPT];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) r[v] = c.template staged<XT>(cur + a.x.off, v);
+    for (int v = 0; v < VPT; ++v) r[v] = c.template staged<XT>(cur, a.x, m, v);
     if (has_y) {
       float factor = a.scale;  // residual scale and the row's 1 / rms
       if (post) {
         float ss[1] = {0.0f};
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-          const F8 y = c.template staged<YT>(cur + a.y.off, v);
+          const F8 y = c.template staged<YT>(cur, a.y, m, v);
           const F2 q = dot8(y, y, f2(0.0f));
           ss[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
         }
@@ -172,19 +195,19 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT < 4 ? 2 : 1)
       }
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        F8 z = c.template staged<YT>(cur + a.y.off, v) * f2(factor);
+        F8 z = c.template staged<YT>(cur, a.y, m, v) * f2(factor);
         if (post) z = z * w_post(v);
         if (kind != E4B_GATE_NONE) {
           F8 f = kind == E4B_GATE_CHANNEL ? (kHold ? hold_gate : c.vector(a.vec_gate, a.gate_f32, v))
                  : kind == E4B_GATE_TOKEN ? fill8(load1(a.vec_gate, m, a.gate_f32))
-                 : a.gate_f32             ? c.template staged<float>(cur + a.gate.off, v)
-                                          : c.template staged<uint16_t>(cur + a.gate.off, v);
+                 : a.gate_f32             ? c.template staged<float>(cur, a.gate, m, v)
+                                          : c.template staged<uint16_t>(cur, a.gate, m, v);
           if (a.sigmoid) f = sigmoid8(f);
           r[v] = fma8(z, f, r[v]);
         } else {
           r[v] = fma8(z, f2(1.0f), r[v]);
         }
-        c.template store<XT>(r_p, v, r[v]);
+        c.template store<XT>(r_p, r_s, v, r[v]);
       }
     }
     if (!next) continue;
@@ -200,34 +223,44 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT < 4 ? 2 : 1)
     for (int v = 0; v < VPT; ++v) {
       const F8 n = r[v] * rstd * w_next(v);
       if (a.n_f32)
-        c.template store<float>(n_p, v, n);
+        c.template store<float>(n_p, n_s, v, n);
       else
-        c.template store<uint16_t>(n_p, v, n);
+        c.template store<uint16_t>(n_p, n_s, v, n);
     }
+  }
+  if constexpr (COLS::kShared) {
+    __syncthreads();
+    flush(odd ^ 1, r_p - a.r.step, n_p - a.n.step);
   }
 }
 
 template <class K>
 cudaError_t launch_kernel(K kernel, const NormArgs& a, const NormShape& s, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
+  const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes + 2 * a.out_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
   kernel<<<s.grid, s.T, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <class XT, class YT, int VPT>
-cudaError_t launch_vec(const NormArgs& a, const NormShape& s, cudaStream_t stream) {
+template <class XT, class YT, int VPT, class COLS>
+cudaError_t launch_cols(const NormArgs& a, const NormShape& s, cudaStream_t stream) {
   const bool all = a.y.p && a.w_next && a.w_post;
-  return all ? launch_kernel(block_norm_forward_vec_kernel<XT, YT, VPT, true>, a, s, stream)
-             : launch_kernel(block_norm_forward_vec_kernel<XT, YT, VPT, false>, a, s, stream);
+  return all ? launch_kernel(block_norm_forward_vec_kernel<XT, YT, VPT, COLS, true>, a, s, stream)
+             : launch_kernel(block_norm_forward_vec_kernel<XT, YT, VPT, COLS, false>, a, s, stream);
+}
+
+template <class XT, class YT, int VPT>
+cudaError_t launch_vec(const NormArgs& a, const NormShape& s, Moved moved, cudaStream_t stream) {
+  return moved == kVector ? launch_cols<XT, YT, VPT, VecCols<VPT>>(a, s, stream)
+                          : launch_cols<XT, YT, VPT, ShiftCols<VPT>>(a, s, stream);
 }
 
 template <class XT, class YT>
-cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  if (vec)
-    return s.vpt == 1   ? launch_vec<XT, YT, 1>(a, s, stream)
-           : s.vpt == 2 ? launch_vec<XT, YT, 2>(a, s, stream)
-                        : launch_vec<XT, YT, 4>(a, s, stream);
+cudaError_t launch_typed(const NormArgs& a, const NormShape& s, Moved moved, cudaStream_t stream) {
+  if (moved != kElements)
+    return s.vpt == 1   ? launch_vec<XT, YT, 1>(a, s, moved, stream)
+           : s.vpt == 2 ? launch_vec<XT, YT, 2>(a, s, moved, stream)
+                        : launch_vec<XT, YT, 4>(a, s, moved, stream);
   // norm_shape() rounds these rows' threads to one of the sizes below.
   if (s.vpt == 4) return launch_kernel(block_norm_forward_kernel<XT, YT, 4, 512>, a, s, stream);
   if (s.vpt == 2) return launch_kernel(block_norm_forward_kernel<XT, YT, 2, 384>, a, s, stream);
@@ -280,44 +313,62 @@ NormShape norm_shape(int64_t M, int H, int threads_per_sm, bool vec) {
 }
 constexpr int kForwardThreads = 768, kBackwardThreads = 768;  // per SM
 
-// How a call's rows can be moved: as vectors of 8 columns, or else in units of 16 bytes.
+// How a call's rows can be moved: as aligned vectors of 8 columns, as shifted ones, or
+// else in units of 16 bytes.
 struct Moves {
-  bool vec, units;
+  bool vec, shift, units;
 };
 
 // The shape, and the ring: as many stages (2 to 4) as leave room for the SM's other
-// CTAs, or, of rows too long for that, none.  Returns whether rows are moved as vectors.
-bool plan(NormArgs* a, NormShape* s, const Moves& moves, bool x_f32, bool y_f32, int threads_per_sm) {
+// CTAs, or, of rows too long for that, none.
+Moved plan(NormArgs* a, NormShape* s, const Moves& moves, bool x_f32, bool y_f32, int threads_per_sm) {
   constexpr uint32_t kRoom = 216 * 1024;
-  bool vec = moves.vec;
-  for (;; vec = false) {
-    *s = norm_shape(a->M, a->H, threads_per_sm, vec);
+  for (const Moved moved : {kVector, kShifted, kElements}) {
+    if ((moved == kVector && !moves.vec) || (moved == kShifted && !moves.shift)) continue;
+    *s = norm_shape(a->M, a->H, threads_per_sm, moved != kElements);
     for (RowDst* d : {&a->r, &a->n, &a->dx, &a->dy}) d->step = d->row * s->grid;
+    const uint32_t columns = s->T * s->vpt * 8;
     uint32_t off = 0;
     auto place = [&](RowSrc* r, bool f32) {
       if (!r->p) return;
       r->row = r->ld * (f32 ? 4 : 2);
       r->step = r->row * s->grid;
       r->off = off;
-      off += vec ? static_cast<uint32_t>(s->T * s->vpt * 8 * (f32 ? 4 : 2))
-                 : static_cast<uint32_t>(align_up(static_cast<size_t>(a->H) * (f32 ? 4 : 2), 16) + 16);
+      // a shifted read reaches up to 32 bytes past its group
+      off += moved == kElements ? static_cast<uint32_t>(align_up(static_cast<size_t>(a->H) * (f32 ? 4 : 2), 16) + 16)
+                                : columns * (f32 ? 4 : 2) + (moved == kShifted ? 32 : 0);
     };
     place(&a->dr, x_f32);
     place(&a->x, x_f32);
     place(&a->dn, a->n_f32);
     place(&a->y, y_f32);
     place(&a->gate, a->gate_f32);
-    const int ctas = std::min(16, std::max(1, threads_per_sm / s->T));
     a->stage_bytes = off;
-    a->stages = static_cast<int>(std::max(2u, std::min(4u, kRoom / ctas / off)));
-    if ((vec || moves.units) && a->stages * off <= kRoom) return vec;
-    if (!vec) break;
+    // Shifted outputs: rows with 16 bytes before and 32 behind them.
+    uint32_t out = 0;
+    auto slot = [&](int i, bool there, bool f32) {
+      a->out_slot[i] = out + 16;
+      if (there && moved == kShifted) out += columns * (f32 ? 4 : 2) + 48;
+    };
+    slot(0, a->r.p || a->dx.p, x_f32);
+    slot(1, a->n.p || a->dy.p, a->n.p ? a->n_f32 : y_f32);
+    slot(2, a->dgate && a->gate.p, a->gate_f32);
+    a->out_bytes = out;
+    const int ctas = std::min(16, std::max(1, threads_per_sm / s->T));
+    const uint32_t each = kRoom / ctas;
+    a->stages = static_cast<int>(std::max(2u, std::min(4u, each > 2 * out ? (each - 2 * out) / off : 0u)));
+    a->out_off = a->stages * off;
+    if ((moved != kElements || moves.units) && a->stages * off + 2 * out <= kRoom) return moved;
   }
   a->stages = 0;
-  return false;
+  a->out_bytes = 0;
+  return kElements;
 }
 
 int64_t size_of(int dtype) { return dtype == E4B_F32 ? 4 : 2; }
+const char* const kForwardPath[] = {"block_norm.forward.scalar", "block_norm.forward.shifted", "block_norm.forward"};
+const char* const kBackwardPath[] = {"block_norm.backward.scalar", "block_norm.backward.shifted", "block_norm.backward"};
+
 bool is_dtype(int d) { return d == E4B_F32 || d == E4B_BF16; }
 bool on_element(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype == E4B_F32 ? 3u : 1u)) == 0;
@@ -355,6 +406,7 @@ e4b_status check_rows(const char* name, const void* p, int dtype, int64_t ld, in
   if (ld < H) return fail(E4B_ERR_INVALID_ARGUMENT, std::string(name) + "'s leading dimension must be >= H");
   if (!on_element(p, dtype)) return fail(E4B_ERR_INVALID_ARGUMENT, std::string(name) + " must be aligned to its elements");
   moves->vec = moves->vec && vec_base(p, dtype) && ld % 8 == 0;
+  moves->shift = moves->shift && aligned16(p);
   moves->units = moves->units && aligned16(p);
   return E4B_OK;
 }
@@ -381,23 +433,27 @@ NormArgs norm_args(const e4b_block_norm* p, int64_t M, const void* y, int64_t ld
   return a;
 }
 
-// Whether weights, gate and (backward) its gradient allow vectors and units.
+// What weights, gate and (backward) its gradient allow.
 Moves moves_of(const e4b_block_norm* p, const void* gate, e4b_gate_kind kind, e4b_dtype gate_dtype, const void* dgate) {
-  Moves m{p->H % 8 == 0 && vec_base(p->w_post, p->w_dtype) && vec_base(p->w_next, p->w_dtype), true};
-  if (kind == E4B_GATE_CHANNEL || kind == E4B_GATE_FULL) m.vec = m.vec && vec_base(gate, gate_dtype);
+  Moves m{};
+  m.shift = vec_base(p->w_post, p->w_dtype) && vec_base(p->w_next, p->w_dtype);
+  if (kind == E4B_GATE_CHANNEL) m.shift = m.shift && vec_base(gate, gate_dtype);
+  m.vec = m.shift && p->H % 8 == 0;
+  m.units = true;
   if (kind == E4B_GATE_FULL) {
-    m.vec = m.vec && vec_base(dgate, gate_dtype);
+    m.vec = m.vec && vec_base(gate, gate_dtype) && vec_base(dgate, gate_dtype);
     m.units = aligned16(gate);
+    m.shift = m.shift && m.units;
   }
   return m;
 }
 
 }  // namespace
 
-cudaError_t launch_block_norm_forward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec,
+cudaError_t launch_block_norm_forward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, Moved moved,
                                       cudaStream_t stream) {
-  if (x_f32) return y_f32 ? launch_typed<float, float>(a, s, vec, stream) : launch_typed<float, uint16_t>(a, s, vec, stream);
-  return y_f32 ? launch_typed<uint16_t, float>(a, s, vec, stream) : launch_typed<uint16_t, uint16_t>(a, s, vec, stream);
+  if (x_f32) return y_f32 ? launch_typed<float, float>(a, s, moved, stream) : launch_typed<float, uint16_t>(a, s, moved, stream);
+  return y_f32 ? launch_typed<uint16_t, float>(a, s, moved, stream) : launch_typed<uint16_t, uint16_t>(a, s, moved, stream);
 }
 
 }  // namespace e4b
@@ -435,11 +491,11 @@ e4b_status e4b_block_norm_forward(const void* x, e4b_dtype x_dtype, int64_t ldx,
   a.n.row = ldn * size_of(n_dtype);
   NormShape s{};
   const bool x_f32 = x_dtype == E4B_F32, y_f32 = y && y_dtype == E4B_F32;
-  const bool vec = plan(&a, &s, moves, x_f32, y_f32, kForwardThreads);
+  const Moved moved = plan(&a, &s, moves, x_f32, y_f32, kForwardThreads);
   LaunchScope ls("block_norm.forward", st);
-  if (cudaError_t err = launch_block_norm_forward(a, x_f32, y_f32, s, vec, st); err != cudaSuccess)
+  if (cudaError_t err = launch_block_norm_forward(a, x_f32, y_f32, s, moved, st); err != cudaSuccess)
     return cuda_fail(err, "block norm forward launch");
-  set_path(vec ? "block_norm.forward" : "block_norm.forward.scalar");
+  set_path(kForwardPath[moved]);
   return E4B_OK;
 }
 
@@ -492,16 +548,16 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
   a.dy.row = lddy * size_of(y_dtype);
   a.dgate = dgate;
   a.partial = static_cast<float*>(workspace);
-  bool vec = false;
+  Moved moved = kElements;
   if (M > 0) {
     NormShape s{};
     const bool x_f32 = x_dtype == E4B_F32, y_f32 = y && y_dtype == E4B_F32;
     // the partial sums' rows are vectors of 32 bytes
     moves.vec = moves.vec && vec_base(workspace, E4B_F32);
-    vec = plan(&a, &s, moves, x_f32, y_f32, kBackwardThreads);
+    moved = plan(&a, &s, moves, x_f32, y_f32, kBackwardThreads);
     a.parts = s.grid;
     LaunchScope ls("block_norm.backward", st);
-    if (cudaError_t err = launch_block_norm_backward(a, x_f32, y_f32, s, vec, st); err != cudaSuccess)
+    if (cudaError_t err = launch_block_norm_backward(a, x_f32, y_f32, s, moved, st); err != cudaSuccess)
       return cuda_fail(err, "block norm backward launch");
   }
   float* dchannel = gate_kind == E4B_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
@@ -511,7 +567,7 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
     block_norm_reduce_kernel<<<dim3((a.H + kRedCols - 1) / kRedCols, 3), dim3(kRedCols, kRedLanes), 0, st>>>(ra);
   }
   if (cudaError_t err = cudaGetLastError(); err != cudaSuccess) return cuda_fail(err, "block norm reduce launch");
-  set_path(M == 0 ? "block_norm.backward.empty" : vec ? "block_norm.backward" : "block_norm.backward.scalar");
+  set_path(M == 0 ? "block_norm.backward.empty" : kBackwardPath[moved]);
   return E4B_OK;
 }
 

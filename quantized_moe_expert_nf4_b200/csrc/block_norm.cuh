@@ -35,6 +35,8 @@ struct NormArgs {
   int H, parts;
   int stages;                        // of the ring; 0: rows are read from memory directly
   uint32_t stage_bytes;
+  uint32_t out_off, out_bytes;       // shifted rows: where the outputs' rows are put together, twice out_bytes
+  uint32_t out_slot[3];
   int gate_kind, gate_f32, sigmoid, w_f32, n_f32;
   float scale, offset, eps, inv_h;
 };
@@ -46,10 +48,13 @@ struct NormShape {
 // Most threads of a CTA, and CTAs an SM should hold, by the groups of a thread.
 constexpr int norm_threads(int vpt) { return vpt == 4 ? 512 : 384; }
 
-// Launchers; vec: all rows can be moved as vectors of 8 columns (the ring is used).
-cudaError_t launch_block_norm_forward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec,
+// How a call's rows are moved.  kVector: 8 columns of every row are aligned vectors.
+// kShifted: rows start anywhere within 16 bytes, the tensors do not.  kElements: all else.
+enum Moved { kElements = 0, kShifted = 1, kVector = 2 };
+
+cudaError_t launch_block_norm_forward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, Moved moved,
                                       cudaStream_t stream);
-cudaError_t launch_block_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec,
+cudaError_t launch_block_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, Moved moved,
                                        cudaStream_t stream);
 
 // ---- pairs of floats --------------------------------------------------------------
@@ -201,10 +206,12 @@ struct VecCols {
       col[v] = in[v] ? at : 0;
     }
   }
+  static constexpr bool kShared = false;  // a thread reads its own places of the ring only
+  __device__ __forceinline__ uint32_t place() const { return threadIdx.x * 16; }
   // Into this thread's places of a ring stage (`dst`: its unit of plane 0) from a
   // row: 8 bf16 are one unit, 8 floats two, in two planes.
   template <class E>
-  __device__ __forceinline__ void fetch(uint32_t dst, const unsigned char* row) const {
+  __device__ __forceinline__ void fetch(uint32_t dst, const unsigned char* row, const RowSrc&, int64_t) const {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const E* src = reinterpret_cast<const E*>(row) + col[v];
@@ -217,7 +224,8 @@ struct VecCols {
     }
   }
   template <class E>
-  __device__ __forceinline__ F8 staged(const unsigned char* src, int v) const {
+  __device__ __forceinline__ F8 staged(const unsigned char* stage, const RowSrc& s, int64_t, int v) const {
+    const unsigned char* src = stage + s.off;
     const uint4 q = *reinterpret_cast<const uint4*>(src + v * T16);
     if constexpr (sizeof(E) == 2) return unpack8(q);
     const uint4 u = *reinterpret_cast<const uint4*>(src + (VPT + v) * T16);
@@ -229,8 +237,116 @@ struct VecCols {
     return f32 ? load8(static_cast<const float*>(p) + col[v]) : load8(static_cast<const uint16_t*>(p) + col[v]);
   }
   template <class E>
-  __device__ __forceinline__ void store(unsigned char* row, int v, const F8& f) const {
+  __device__ __forceinline__ void store(unsigned char* row, unsigned char*, int v, const F8& f) const {
     if (in[v]) store8(reinterpret_cast<E*>(row) + col[v], f);
+  }
+  template <class E>
+  __device__ __forceinline__ void sums(E* row, int v, const F8& f) const {
+    if (in[v]) store8(row + col[v], f);
+  }
+};
+
+// ---- rows that start anywhere within 16 bytes ----------------------------------------------
+// The 16 bytes that start `by` (even, 0 .. 14) bytes after the 16-byte aligned p.
+__device__ __forceinline__ uint4 raw16(const unsigned char* p, uint32_t by) {
+  const uint2* q = reinterpret_cast<const uint2*>(p + (by & 8));
+  const uint2 a = q[0], b = q[1], c = q[2];
+  const bool s = by & 4;
+  const uint32_t v0 = s ? a.y : a.x, v1 = s ? b.x : a.y, v2 = s ? b.y : b.x, v3 = s ? c.x : b.y, v4 = s ? c.y : c.x;
+  const uint32_t h = (by & 2) * 8;
+  return make_uint4(__funnelshift_r(v0, v1, h), __funnelshift_r(v1, v2, h), __funnelshift_r(v2, v3, h), __funnelshift_r(v3, v4, h));
+}
+
+// The same groups of 8 columns as VecCols, of rows whose first byte lies anywhere in a
+// 16-byte unit.  A row comes into the ring as the units that it touches and is
+// read across threads, shifted; an output row is put together in shared memory and
+// written in the units of its own place one row later, its first and last
+// units by element.  The last group of a row may be a part: its columns past H are zero.
+template <int VPT>
+struct ShiftCols {
+  int T, H;
+  int col[VPT], count[VPT];  // first column of each group, its columns (0 .. 8)
+  bool in[VPT];
+  static constexpr bool kShared = true;
+  __device__ __forceinline__ ShiftCols(int T_, int t, int H_) : T(T_), H(H_) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      col[v] = (v * T + t) * 8;
+      count[v] = max(0, min(8, H - col[v]));
+      in[v] = count[v] > 0;
+    }
+  }
+  __device__ __forceinline__ uint32_t place() const { return 0; }
+  static __device__ __forceinline__ uint32_t lead_of(const void* row) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) & 15u; }
+  __device__ __forceinline__ F8 cut(F8 f, int v) const {
+    if (count[v] < 8) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        f.p[q] = f2(2 * q < count[v] ? lo(f.p[q]) : 0.0f, 2 * q + 1 < count[v] ? hi(f.p[q]) : 0.0f);
+    }
+    return f;
+  }
+  // `last`: rows behind this one.  Nothing past the tensor's end is read.
+  template <class E>
+  __device__ __forceinline__ void fetch(uint32_t dst, const unsigned char* row, const RowSrc& s, int64_t last) const {
+    const uint32_t lead = lead_of(row);
+    const int bytes = static_cast<int>(lead) + H * static_cast<int>(sizeof(E));
+    const unsigned char* src = row - lead;
+    const int64_t left = last * s.row + bytes;  // to the tensor's end
+    const int safe = left >= bytes + 15 ? bytes + 15 : static_cast<int>(left);
+    for (int u = threadIdx.x * 16; u < bytes; u += T * 16) cp16(dst + u, src + u, min(16, safe - u));
+  }
+  template <class E>
+  __device__ __forceinline__ F8 staged(const unsigned char* stage, const RowSrc& s, int64_t m, int v) const {
+    const uint32_t lead = (lead_of(s.p) + static_cast<uint32_t>(m) * static_cast<uint32_t>(s.row)) & 15u;
+    const unsigned char* src = stage + s.off + col[v] * static_cast<int>(sizeof(E));
+    const uint4 q = raw16(src, lead);
+    if constexpr (sizeof(E) == 2) return cut(unpack8(q), v);
+    const uint4 u = raw16(src + 16, lead);
+    return cut({{f2(__uint_as_float(q.x), __uint_as_float(q.y)), f2(__uint_as_float(q.z), __uint_as_float(q.w)),
+                 f2(__uint_as_float(u.x), __uint_as_float(u.y)), f2(__uint_as_float(u.z), __uint_as_float(u.w))}}, v);
+  }
+  __device__ __forceinline__ F8 vector(const void* p, int f32, int v) const {
+    if (count[v] == 8)
+      return f32 ? load8(static_cast<const float*>(p) + col[v]) : load8(static_cast<const uint16_t*>(p) + col[v]);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < count[v] ? load1(p, col[v] + j, f32) : 0.0f;
+    return set8(f);
+  }
+  // Into the row being put together at `slot`.
+  template <class E>
+  __device__ __forceinline__ void store(unsigned char*, unsigned char* slot, int v, const F8& f) const {
+    if (!in[v]) return;
+    uint4* to = reinterpret_cast<uint4*>(slot + col[v] * static_cast<int>(sizeof(E)));
+    if constexpr (sizeof(E) == 2) {
+      *to = make_uint4(pack_bf16x2(lo(f.p[0]), hi(f.p[0])), pack_bf16x2(lo(f.p[1]), hi(f.p[1])),
+                       pack_bf16x2(lo(f.p[2]), hi(f.p[2])), pack_bf16x2(lo(f.p[3]), hi(f.p[3])));
+    } else {
+      to[0] = make_uint4(__float_as_uint(lo(f.p[0])), __float_as_uint(hi(f.p[0])), __float_as_uint(lo(f.p[1])), __float_as_uint(hi(f.p[1])));
+      to[1] = make_uint4(__float_as_uint(lo(f.p[2])), __float_as_uint(hi(f.p[2])), __float_as_uint(lo(f.p[3])), __float_as_uint(hi(f.p[3])));
+    }
+  }
+  // The row put together at `slot` to its place in memory.
+  template <class E>
+  __device__ __forceinline__ void flush(unsigned char* row, const unsigned char* slot) const {
+    const uint32_t lead = lead_of(row);
+    const int bytes = static_cast<int>(lead) + H * static_cast<int>(sizeof(E));
+    const uint32_t by = (16u - lead) & 15u;
+    for (int u = threadIdx.x * 16; u < bytes; u += T * 16) {
+      if (u >= static_cast<int>(lead) && u + 16 <= bytes) {
+        *reinterpret_cast<uint4*>(row - lead + u) = raw16(slot + u - (lead ? 16 : 0), by);
+      } else {
+        for (int b = max(u, static_cast<int>(lead)); b < min(u + 16, bytes); b += sizeof(E))
+          *reinterpret_cast<E*>(row - lead + b) = *reinterpret_cast<const E*>(slot + b - lead);
+      }
+    }
+  }
+  template <class E>
+  __device__ __forceinline__ void sums(E* row, int v, const F8& f) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < count[v]) row[col[v] + j] = get8(f, j);
   }
 };
 

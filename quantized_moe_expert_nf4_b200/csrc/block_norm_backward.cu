@@ -102,52 +102,54 @@ __global__ void __launch_bounds__(T, VPT == 1 ? 768 / T : 1)
   }
 }
 
-// Rows moved as vectors.  ALL: y, both weights, dr, dx and dy are there, the step
+// Rows moved as vectors, aligned or shifted (COLS).  ALL: y, both weights, dr, dx and dy are there, the step
 // between two blocks in training; what each row would ask of them at run time
 // costs about a third of the kernel's instructions.
-template <class XT, class YT, int VPT, bool ALL>
+template <class XT, class YT, int VPT, class COLS, bool ALL>
 __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     block_norm_backward_vec_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float red[2][2][64];  // as above
   const int T = blockDim.x;
-  const VecCols<VPT> c(T, threadIdx.x, a.H);
+  const COLS c(T, threadIdx.x, a.H);
   const bool has_y = ALL || a.y.p, next = ALL || a.w_next, post = ALL || a.w_post;
   const bool has_dr = ALL || a.dr.p, has_dx = ALL || a.dx.p, has_dy = ALL || a.dy.p;
   const int kind = a.gate_kind, stages = a.stages;
   const int step = static_cast<int>(gridDim.x);
   auto row_of = [&](const RowSrc& t) { return static_cast<const unsigned char*>(t.p) + blockIdx.x * t.row; };
   const unsigned char *r_p = row_of(a.x), *dr_p = row_of(a.dr), *y_p = row_of(a.y), *dn_p = row_of(a.dn), *g_p = row_of(a.gate);
-  const uint32_t ring_u = smem_addr(ring) + threadIdx.x * 16;
-  const unsigned char* ring_p = ring + threadIdx.x * 16;
+  const uint32_t ring_u = smem_addr(ring) + c.place();
+  const unsigned char* ring_p = ring + c.place();
   int64_t put_row = blockIdx.x;
   int put_stage = 0, stage = 0;
-  // A thread reads its own places only, so that filling the last row's stage needs no barrier.
+  // Aligned: a thread reads its own places only, so that filling the last row's stage
+  // needs no barrier.  Shifted: see below.
   auto put = [&]() {
     if (put_row < a.M) {
+      const int64_t last = a.M - 1 - put_row;
       const uint32_t to = ring_u + put_stage * a.stage_bytes;
       if (next) {
-        c.template fetch<XT>(to + a.x.off, r_p);
+        c.template fetch<XT>(to + a.x.off, r_p, a.x, last);
         if (a.n_f32)
-          c.template fetch<float>(to + a.dn.off, dn_p);
+          c.template fetch<float>(to + a.dn.off, dn_p, a.dn, last);
         else
-          c.template fetch<uint16_t>(to + a.dn.off, dn_p);
+          c.template fetch<uint16_t>(to + a.dn.off, dn_p, a.dn, last);
         r_p += a.x.step;
         dn_p += a.dn.step;
       }
       if (has_y) {
-        c.template fetch<YT>(to + a.y.off, y_p);
+        c.template fetch<YT>(to + a.y.off, y_p, a.y, last);
         y_p += a.y.step;
       }
       if (has_dr) {
-        c.template fetch<XT>(to + a.dr.off, dr_p);
+        c.template fetch<XT>(to + a.dr.off, dr_p, a.dr, last);
         dr_p += a.dr.step;
       }
       if (kind == E4B_GATE_FULL) {
         if (a.gate_f32)
-          c.template fetch<float>(to + a.gate.off, g_p);
+          c.template fetch<float>(to + a.gate.off, g_p, a.gate, last);
         else
-          c.template fetch<uint16_t>(to + a.gate.off, g_p);
+          c.template fetch<uint16_t>(to + a.gate.off, g_p, a.gate, last);
         g_p += a.gate.step;
       }
       put_row += step;
@@ -160,16 +162,41 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
   F8 s_post[VPT], s_next[VPT], s_gate[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) s_post[v] = s_next[v] = s_gate[v] = zero8();
+  auto flush = [&](int set, int64_t m, unsigned char* dx_row, unsigned char* dy_row) {
+    if constexpr (COLS::kShared) {
+      const unsigned char* out = ring + a.out_off + set * a.out_bytes;
+      if (has_dx) c.template flush<XT>(dx_row, out + a.out_slot[0]);
+      if (has_y && has_dy) c.template flush<YT>(dy_row, out + a.out_slot[1]);
+      if (kind == E4B_GATE_FULL && a.dgate) {
+        unsigned char* row = static_cast<unsigned char*>(a.dgate) + m * a.gate.row;
+        if (a.gate_f32)
+          c.template flush<float>(row, out + a.out_slot[2]);
+        else
+          c.template flush<uint16_t>(row, out + a.out_slot[2]);
+      }
+    }
+  };
   int odd = 0;
+  int64_t m_last = -1;
   unsigned char* dx_p = static_cast<unsigned char*>(a.dx.p) + blockIdx.x * a.dx.row;
   unsigned char* dy_p = static_cast<unsigned char*>(a.dy.p) + blockIdx.x * a.dy.row;
   for (int64_t m = blockIdx.x; m < a.M; m += step, odd ^= 1, dx_p += a.dx.step, dy_p += a.dy.step) {
+    m_last = m;
     cp_wait(stages);
+    unsigned char *dx_s = nullptr, *dy_s = nullptr, *dg_s = nullptr;
+    if constexpr (COLS::kShared) {
+      // The copies are in and the last row is done with: its stage and its outputs' rows.
+      // Two sets of output rows: one is written while the other is put together.
+      __syncthreads();
+      unsigned char* out = ring + a.out_off + odd * a.out_bytes;
+      dx_s = out + a.out_slot[0], dy_s = out + a.out_slot[1], dg_s = out + a.out_slot[2];
+      if (m != blockIdx.x) flush(odd ^ 1, m - step, dx_p - a.dx.step, dy_p - a.dy.step);
+    }
     put();
     const unsigned char* cur = ring_p + stage * a.stage_bytes;
     stage = stage + 1 == stages ? 0 : stage + 1;
     auto load_dn = [&](int v) {
-      return a.n_f32 ? c.template staged<float>(cur + a.dn.off, v) : c.template staged<uint16_t>(cur + a.dn.off, v);
+      return a.n_f32 ? c.template staged<float>(cur, a.dn, m, v) : c.template staged<uint16_t>(cur, a.dn, m, v);
     };
     float s1[3] = {0.0f, 0.0f, 0.0f};  // sums of r^2, h * r, y^2
     F8 h[VPT];
@@ -177,12 +204,12 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     for (int v = 0; v < VPT; ++v) {
       const F2 z = f2(0.0f);
       if (has_y) {
-        const F8 y = c.template staged<YT>(cur + a.y.off, v);
+        const F8 y = c.template staged<YT>(cur, a.y, m, v);
         const F2 q = dot8(y, y, z);
         s1[2] += c.in[v] ? lo(q) + hi(q) : 0.0f;
       }
       if (next) {
-        const F8 r = c.template staged<XT>(cur + a.x.off, v);
+        const F8 r = c.template staged<XT>(cur, a.x, m, v);
         h[v] = load_dn(v) * (c.vector(a.w_next, a.w_f32, v) + offset);
         const F2 q = dot8(r, r, z), u = dot8(h[v], r, z);
         s1[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
@@ -196,22 +223,22 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     float s2[2] = {0.0f, 0.0f};  // sums of k * yhat, d * z * slope
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      F8 d = has_dr ? c.template staged<XT>(cur + a.dr.off, v) : zero8();
+      F8 d = has_dr ? c.template staged<XT>(cur, a.dr, m, v) : zero8();
       if (next) {
-        const F8 hat = c.template staged<XT>(cur + a.x.off, v) * f2(rstd_r);
+        const F8 hat = c.template staged<XT>(cur, a.x, m, v) * f2(rstd_r);
         s_next[v] = fma8(load_dn(v), hat, s_next[v]);
         d = fma8(fma8(hat, f2(-mean_r), h[v]), f2(rstd_r), d);
       }
-      if (has_dx) c.template store<XT>(dx_p, v, d);
+      if (has_dx) c.template store<XT>(dx_p, dx_s, v, d);
       if (!has_y) continue;
-      const F8 hat = c.template staged<YT>(cur + a.y.off, v) * f2(rstd_y);
+      const F8 hat = c.template staged<YT>(cur, a.y, m, v) * f2(rstd_y);
       const F8 w = post ? c.vector(a.w_post, a.w_f32, v) + offset : fill8(1.0f);
       F8 dz = d * f2(a.scale);
       if (kind != E4B_GATE_NONE) {
         F8 f = kind == E4B_GATE_CHANNEL ? c.vector(a.vec_gate, a.gate_f32, v)
                : kind == E4B_GATE_TOKEN ? fill8(load1(a.vec_gate, m, a.gate_f32))
-               : a.gate_f32             ? c.template staged<float>(cur + a.gate.off, v)
-                                        : c.template staged<uint16_t>(cur + a.gate.off, v);
+               : a.gate_f32             ? c.template staged<float>(cur, a.gate, m, v)
+                                        : c.template staged<uint16_t>(cur, a.gate, m, v);
         F8 dg = dz * (hat * w);
         if (a.sigmoid) {
           f = sigmoid8(f);
@@ -227,9 +254,9 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
         } else if (a.dgate) {
           unsigned char* row = static_cast<unsigned char*>(a.dgate) + m * a.gate.row;
           if (a.gate_f32)
-            c.template store<float>(row, v, dg);
+            c.template store<float>(row, dg_s, v, dg);
           else
-            c.template store<uint16_t>(row, v, dg);
+            c.template store<uint16_t>(row, dg_s, v, dg);
         }
       }
       s_post[v] = fma8(dz, hat, s_post[v]);
@@ -244,39 +271,49 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      c.template store<YT>(dy_p, v, fma8(c.template staged<YT>(cur + a.y.off, v), f2(-mean_y), k[v]) * f2(rstd_y));
+      c.template store<YT>(dy_p, dy_s, v, fma8(c.template staged<YT>(cur, a.y, m, v), f2(-mean_y), k[v]) * f2(rstd_y));
+  }
+  if constexpr (COLS::kShared) {
+    __syncthreads();
+    flush(odd ^ 1, m_last, dx_p - a.dx.step, dy_p - a.dy.step);
   }
   const int64_t plane = static_cast<int64_t>(a.parts) * a.H;
-  auto part = [&](int q) { return reinterpret_cast<unsigned char*>(a.partial + q * plane + static_cast<int64_t>(blockIdx.x) * a.H); };
+  float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.H;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    if (post) c.template store<float>(part(0), v, s_post[v]);
-    if (next) c.template store<float>(part(1), v, s_next[v]);
-    if (kind == E4B_GATE_CHANNEL) c.template store<float>(part(2), v, s_gate[v]);
+    if (post) c.sums(part, v, s_post[v]);
+    if (next) c.sums(part + plane, v, s_next[v]);
+    if (kind == E4B_GATE_CHANNEL) c.sums(part + 2 * plane, v, s_gate[v]);
   }
 }
 
 template <class K>
 cudaError_t launch_kernel(K kernel, const NormArgs& a, const NormShape& s, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes;
+  const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes + 2 * a.out_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
   kernel<<<s.grid, s.T, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <class XT, class YT, int VPT>
-cudaError_t launch_vec(const NormArgs& a, const NormShape& s, cudaStream_t stream) {
+template <class XT, class YT, int VPT, class COLS>
+cudaError_t launch_cols(const NormArgs& a, const NormShape& s, cudaStream_t stream) {
   const bool all = a.y.p && a.w_next && a.w_post && a.dr.p && a.dx.p && a.dy.p;
-  return all ? launch_kernel(block_norm_backward_vec_kernel<XT, YT, VPT, true>, a, s, stream)
-             : launch_kernel(block_norm_backward_vec_kernel<XT, YT, VPT, false>, a, s, stream);
+  return all ? launch_kernel(block_norm_backward_vec_kernel<XT, YT, VPT, COLS, true>, a, s, stream)
+             : launch_kernel(block_norm_backward_vec_kernel<XT, YT, VPT, COLS, false>, a, s, stream);
+}
+
+template <class XT, class YT, int VPT>
+cudaError_t launch_vec(const NormArgs& a, const NormShape& s, Moved moved, cudaStream_t stream) {
+  return moved == kVector ? launch_cols<XT, YT, VPT, VecCols<VPT>>(a, s, stream)
+                          : launch_cols<XT, YT, VPT, ShiftCols<VPT>>(a, s, stream);
 }
 
 template <class XT, class YT>
-cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaStream_t stream) {
-  if (vec)
-    return s.vpt == 1   ? launch_vec<XT, YT, 1>(a, s, stream)
-           : s.vpt == 2 ? launch_vec<XT, YT, 2>(a, s, stream)
-                        : launch_vec<XT, YT, 4>(a, s, stream);
+cudaError_t launch_typed(const NormArgs& a, const NormShape& s, Moved moved, cudaStream_t stream) {
+  if (moved != kElements)
+    return s.vpt == 1   ? launch_vec<XT, YT, 1>(a, s, moved, stream)
+           : s.vpt == 2 ? launch_vec<XT, YT, 2>(a, s, moved, stream)
+                        : launch_vec<XT, YT, 4>(a, s, moved, stream);
   // norm_shape() rounds these rows' threads to one of the sizes below.
   if (s.vpt == 4) return launch_kernel(block_norm_backward_kernel<XT, YT, 4, 512>, a, s, stream);
   if (s.vpt == 2) return launch_kernel(block_norm_backward_kernel<XT, YT, 2, 384>, a, s, stream);
@@ -288,10 +325,10 @@ cudaError_t launch_typed(const NormArgs& a, const NormShape& s, bool vec, cudaSt
 
 }  // namespace
 
-cudaError_t launch_block_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, bool vec,
+cudaError_t launch_block_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, const NormShape& s, Moved moved,
                                        cudaStream_t stream) {
-  if (x_f32) return y_f32 ? launch_typed<float, float>(a, s, vec, stream) : launch_typed<float, uint16_t>(a, s, vec, stream);
-  return y_f32 ? launch_typed<uint16_t, float>(a, s, vec, stream) : launch_typed<uint16_t, uint16_t>(a, s, vec, stream);
+  if (x_f32) return y_f32 ? launch_typed<float, float>(a, s, moved, stream) : launch_typed<float, uint16_t>(a, s, moved, stream);
+  return y_f32 ? launch_typed<uint16_t, float>(a, s, moved, stream) : launch_typed<uint16_t, uint16_t>(a, s, moved, stream);
 }
 
 }  // namespace e4b

@@ -133,11 +133,11 @@ def test_types_and_strides(x, y, w, n, g_dtype, H, pad):
     require_gpu()
     t, norm, ref = _inputs(6, H, "full", True, x=x, y=y, w=w, n=n, g_dtype=g_dtype, pad=pad)
     _check_forward(t, norm, ref, n_dtype=n, pad=pad)
-    assert e4b.last_path() == ("block_norm.forward" if H % 8 == 0 and pad % 8 == 0 else "block_norm.forward.scalar")
+    assert e4b.last_path() == ("block_norm.forward" if H % 8 == 0 and pad % 8 == 0 else "block_norm.forward.shifted")
     _check_backward(t, norm, ref)
 
 
-def test_unaligned_bases_take_the_scalar_path():
+def test_unaligned_bases_are_read_by_element():
     require_gpu()
     t, norm, ref = _inputs(4, 128)
     buf = torch.zeros(4 * 128 + 1, dtype=BF, device="cuda")
