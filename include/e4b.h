@@ -506,9 +506,9 @@ typedef struct {
  * x [M, ldx] bf16 (ldx >= K, ldx % 8 == 0); out [M, ldo] of out_dtype.
  * Requires K a multiple of the group; any N >= 1, even with SwiGLU;
  * 0 <= M <= 16 (longer inputs: e4b_grouped_4bit_gemm() with one group).
- * fp32 accumulation; scales multiply group sums in fp32.  With bf16 output the
- * NF4 and FP4 entries are rounded to bf16, as in the grouped GEMM; with fp32
- * output they are exact to 2^-17.  Deterministic.  No workspace.
+ * fp32 accumulation; scales multiply group sums in fp32.  INT4 and FP4 values
+ * are exact; NF4 entries are within 1.8e-3 with bf16 output and 2^-17 with
+ * fp32 output.  Deterministic.  No workspace.
  */
 E4B_API e4b_status e4b_gemv_4bit(const uint16_t* x, int64_t M, int64_t ldx, const e4b_group_weight* w,
                                  e4b_epilogue epi, void* out, e4b_dtype out_dtype, int64_t ldo,

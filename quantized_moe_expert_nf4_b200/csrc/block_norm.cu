@@ -311,7 +311,7 @@ NormShape norm_shape(int64_t M, int H, int threads_per_sm, bool vec) {
   s.grid = static_cast<int>(std::min<int64_t>(M, kSms * per_sm));
   return s;
 }
-constexpr int kForwardThreads = 768, kBackwardThreads = 768;  // per SM
+constexpr int kForwardThreads = 900, kBackwardThreads = 768;  // per SM
 
 // How a call's rows can be moved: as aligned vectors of 8 columns, as shifted ones, or
 // else in units of 16 bytes.

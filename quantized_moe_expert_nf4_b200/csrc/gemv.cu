@@ -22,9 +22,13 @@
 // Codes become exact bf16 values: int4 by or-ing the code into the mantissa of
 // 128 and subtracting 128 + zero, both exact; codebook entries by byte permutes over their bf16
 // bytes.  Products and group sums are fp32 in the MMA, the scales
-// multiply the group sums in fp32.  With fp32 output a codebook entry is taken as
-// the sum of two bf16 values (error 2^-18 of the entry instead of 2^-9); with bf16
-// output the first alone, whose rounding stays below the output's.
+// multiply the group sums in fp32.  A codebook is taken times a factor, and the scales
+// over it, at which its entries fall nearer to bf16 values: 6 for FP4 (e2m1 values,
+// exact), 1.43672 for NF4 (of all factors the one with the least error over the codes
+// of Gaussian weights in blocks of 64: 0.78e-3 of the weights' rms instead of
+// 1.36e-3, and 1.7e-3 of an entry at most instead of 3.1e-3).  With fp32 output an NF4
+// entry is the sum of two bf16 values (2^-17 of it at most); with bf16 output the
+// first alone, whose rounding stays below the output's.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -48,6 +52,7 @@ struct Params {
   int kw;         // warps that share a row tile
   int split;      // CTAs of a cluster that share a row tile
   int tiles;      // CTA tiles of 16 RT * (8 / kw) rows
+  float book, over_book;  // the codebook's factor, and what the scales take of it
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -227,8 +232,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int64_t at = s_row[j][h] + (in ? grp : 0);
-            const float v = a.scale_f32 ? static_cast<const float*>(a.scales)[at]
-                                        : bf16_bits_to_float(static_cast<const uint16_t*>(a.scales)[at]);
+            float v = a.scale_f32 ? static_cast<const float*>(a.scales)[at]
+                                  : bf16_bits_to_float(static_cast<const uint16_t*>(a.scales)[at]);
+            if constexpr (FMT == kFmtCodebook) v *= p.over_book;
             ns[j][h][i] = in ? v : 0.0f;
             if constexpr (FMT == kFmtInt4)
               if (a.zeros) nz[j][h][i] = a.zeros[at] & 15u;
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   if constexpr (FMT == kFmtCodebook) {
     // Entry b: the pair of codes (b / 16, b % 16); thread b writes its 32 copies.
     static_assert(kWarps * 32 == 256, "a thread per entry");
-    const float hi = codebook_entry(a.quant, threadIdx.x >> 4), lo = codebook_entry(a.quant, threadIdx.x & 15);
+    const float hi = p.book * codebook_entry(a.quant, threadIdx.x >> 4), lo = p.book * codebook_entry(a.quant, threadIdx.x & 15);
     const uint32_t pair = pack_bf16x2(hi, lo);
     const uint32_t rest = pack_bf16x2(hi - __uint_as_float(pair << 16), lo - __uint_as_float(pair & 0xffff0000u));
 #pragma unroll
@@ -481,6 +487,8 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
   p.chunks = static_cast<int>((a.row_bytes + 127) / 128);
+  p.book = a.quant == E4B_QUANT_FP4 ? 6.0f : 1.43672f;
+  p.over_book = 1.0f / p.book;
   const int slots = 2 * di.sm_count;  // two CTAs fit an SM
   const int row_tiles = a.epi == kGemvNone ? (a.N + 15) / 16 : (a.N / 2 + 7) / 8;
   // Two row tiles per warp share the tokens' registers; worth it once every warp
@@ -506,7 +514,7 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, slots);
   if (a.fmt == kGemvBf16) return launch_rows<kFmtBf16, 1, false>(p, rt, grid, stream);
   if (a.fmt == kGemvInt4) return launch_group<kFmtInt4, false>(p, rt, grid, stream);
-  return a.out_f32 ? launch_group<kFmtCodebook, true>(p, rt, grid, stream)
+  return a.out_f32 && a.quant != E4B_QUANT_FP4 ? launch_group<kFmtCodebook, true>(p, rt, grid, stream)
                    : launch_group<kFmtCodebook, false>(p, rt, grid, stream);
 }
 
