@@ -479,6 +479,13 @@ E4B_API e4b_status e4b_moe_expert_forward_decode_noalloc(const uint16_t* x, int6
                                                          uint16_t* out, e4b_stream stream);
 
 /*
+ * The calls from here on are launched so that their start-up overlaps the end
+ * of the work ahead of them on the stream (programmatic dependent launch); they
+ * touch memory only when that work has ended, so the stream's order holds for
+ * everything a caller can see, in CUDA graphs as well.
+ */
+
+/*
  * A dense 4-bit matrix with group scales: the projections and the shared
  * expert of a model whose routed experts are the stacks above.
  * Source: experts4bit-qlora 0.22.0, "Inference" (a fused 4-bit GEMV for single-token
@@ -508,7 +515,7 @@ typedef struct {
  * 0 <= M <= 16 (longer inputs: e4b_grouped_4bit_gemm() with one group).
  * fp32 accumulation; scales multiply group sums in fp32.  INT4 and FP4 values
  * are exact; NF4 entries are within 1.8e-3 with bf16 output and 2^-17 with
- * fp32 output.  Deterministic.  No workspace.
+ * fp32 output.  Deterministic.  No workspace.  out may not overlap x.
  */
 E4B_API e4b_status e4b_gemv_4bit(const uint16_t* x, int64_t M, int64_t ldx, const e4b_group_weight* w,
                                  e4b_epilogue epi, void* out, e4b_dtype out_dtype, int64_t ldo,
@@ -608,6 +615,7 @@ typedef struct {
  * x [M, ldx] bf16 (ldx >= H, ldx % 8 == 0), out [M, H] bf16.  pre [M, 2I]
  * bf16, or NULL: the pre-activations, which the backward needs.  Any M >= 0.
  * fp32 accumulation; h (and pre) are rounded to bf16 once.  Two launches.
+ * Here and in the backward no output may overlap an input or another output.
  * workspace  e4b_gated_ffn_forward_workspace_size() bytes, error word first.
  */
 E4B_API size_t e4b_gated_ffn_forward_workspace_size(int64_t M, const e4b_gated_ffn* w);

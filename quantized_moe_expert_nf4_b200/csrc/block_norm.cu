@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(T, VPT == 1 ? 768 / T : 1)
   // barrier before the next row's.
   __shared__ float red[2][2][64];
   const Cols<VPT, T> c{static_cast<int>(threadIdx.x), a.H};
+  pdl_wait();
+  pdl_launch_dependents();
   Rows<XT, YT, VPT, T, false> rows(a, c, ring);
   const F2 offset = f2(a.offset);
   int odd = 0;
@@ -136,6 +138,8 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT < 4 ? 2 : 1)
     cp_commit();
     put_stage = put_stage + 1 == stages ? 0 : put_stage + 1;
   };
+  pdl_wait();
+  pdl_launch_dependents();
   for (int i = 0; i + 1 < stages; ++i) put();
   const F2 offset = f2(a.offset);
   // One group per thread: its weights and channel gate stay in registers.
@@ -238,8 +242,7 @@ template <class K>
 cudaError_t launch_kernel(K kernel, const NormArgs& a, const NormShape& s, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes + 2 * a.out_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
-  kernel<<<s.grid, s.T, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, s.grid, s.T, smem, 1, stream, a);
 }
 
 template <class XT, class YT, int VPT, class COLS>
@@ -280,20 +283,24 @@ struct ReduceArgs {
 constexpr int kRedCols = 32, kRedLanes = 32;
 
 __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel(ReduceArgs a) {
-  float* out = a.out[blockIdx.y];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x % kRedCols, row = threadIdx.x / kRedCols;
+  const int blocks = (a.H + kRedCols - 1) / kRedCols, which = blockIdx.x / blocks, block = blockIdx.x % blocks;
+  float* out = a.out[which];
   if (!out) return;
   __shared__ float s[kRedLanes][kRedCols];
-  const int col = blockIdx.x * kRedCols + threadIdx.x;
+  const int col = block * kRedCols + lane;
   float sum = 0.0f;
   if (col < a.H) {
-    const float* p = a.partial + static_cast<int64_t>(blockIdx.y) * a.parts * a.H + col;
+    const float* p = a.partial + static_cast<int64_t>(which) * a.parts * a.H + col;
 #pragma unroll 8
-    for (int i = threadIdx.y; i < a.parts; i += kRedLanes) sum += p[static_cast<int64_t>(i) * a.H];
+    for (int i = row; i < a.parts; i += kRedLanes) sum += p[static_cast<int64_t>(i) * a.H];
   }
-  s[threadIdx.y][threadIdx.x] = sum;
+  s[row][lane] = sum;
   __syncthreads();
-  if (threadIdx.y == 0 && col < a.H) {
-    for (int i = 1; i < kRedLanes; ++i) sum += s[i][threadIdx.x];
+  if (row == 0 && col < a.H) {
+    for (int i = 1; i < kRedLanes; ++i) sum += s[i][lane];
     out[col] = sum;
   }
 }
@@ -564,9 +571,11 @@ e4b_status e4b_block_norm_backward(const void* dr, int64_t lddr, const void* dn,
   if (dw_post || dw_next || dchannel) {
     ReduceArgs ra{a.partial, {dw_post, dw_next, dchannel}, a.parts, a.H};
     LaunchScope ls("block_norm.reduce", st);
-    block_norm_reduce_kernel<<<dim3((a.H + kRedCols - 1) / kRedCols, 3), dim3(kRedCols, kRedLanes), 0, st>>>(ra);
+    if (cudaError_t err = launch_overlapped(block_norm_reduce_kernel, 3 * ((a.H + kRedCols - 1) / kRedCols), kRedCols * kRedLanes, 0,
+                                            1, st, ra);
+        err != cudaSuccess)
+      return cuda_fail(err, "block norm reduce launch");
   }
-  if (cudaError_t err = cudaGetLastError(); err != cudaSuccess) return cuda_fail(err, "block norm reduce launch");
   set_path(M == 0 ? "block_norm.backward.empty" : kBackwardPath[moved]);
   return E4B_OK;
 }

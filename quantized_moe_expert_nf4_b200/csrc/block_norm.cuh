@@ -2,6 +2,7 @@
 // translation units).
 #pragma once
 
+#include "async.cuh"
 #include "common.cuh"
 #include "e4b_internal.h"
 

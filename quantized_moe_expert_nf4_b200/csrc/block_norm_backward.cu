@@ -13,6 +13,8 @@ __global__ void __launch_bounds__(T, VPT == 1 ? 768 / T : 1)
   // barrier before the next row's.
   __shared__ float red[2][2][64];
   const Cols<VPT, T> c{static_cast<int>(threadIdx.x), a.H};
+  pdl_wait();
+  pdl_launch_dependents();
   Rows<XT, YT, VPT, T, true> rows(a, c, ring);
   const bool has_y = a.y.p != nullptr, next = a.w_next != nullptr, post = a.w_post != nullptr;
   const int kind = a.gate_kind;
@@ -157,6 +159,8 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     cp_commit();
     put_stage = put_stage + 1 == stages ? 0 : put_stage + 1;
   };
+  pdl_wait();
+  pdl_launch_dependents();
   for (int i = 0; i + 1 < stages; ++i) put();
   const F2 offset = f2(a.offset);
   F8 s_post[VPT], s_next[VPT], s_gate[VPT];
@@ -291,8 +295,7 @@ template <class K>
 cudaError_t launch_kernel(K kernel, const NormArgs& a, const NormShape& s, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(a.stages) * a.stage_bytes + 2 * a.out_bytes;
   if (cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem); err != cudaSuccess) return err;
-  kernel<<<s.grid, s.T, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, s.grid, s.T, smem, 1, stream, a);
 }
 
 template <class XT, class YT, int VPT, class COLS>

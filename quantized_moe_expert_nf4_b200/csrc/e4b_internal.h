@@ -284,6 +284,31 @@ cudaError_t device_info(DeviceInfo* out);
 // raised, under a lock, so a call needing less never lowers what another relies on.
 cudaError_t ensure_smem_limit(const void* func, size_t bytes);
 
+// Launches `kernel` so that it may start before the launch ahead of it in the stream has
+// ended (programmatic dependent launch): its CTAs take free SMs and set themselves up,
+// and it reads and writes nothing in memory before its own pdl_wait(), which returns when
+// all earlier work has ended and is visible.  Every kernel launched like this calls
+// pdl_wait() and then pdl_launch_dependents(): the next may start once all CTAs
+// run and everything before this kernel has ended.  `cluster`: CTAs of a cluster.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), int grid, int block, size_t smem, int cluster, cudaStream_t stream,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace e4b

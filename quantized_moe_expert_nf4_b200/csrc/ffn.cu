@@ -48,15 +48,13 @@ constexpr uint32_t kSmemMax = 227 * 1024;
 
 enum Epi { kEpiPlain = 0, kEpiGlu = 1, kEpiDglu = 2 };
 
-// The products of one call are launched so that one may start before the last has
-// ended (programmatic dependent launch).  kAfterAll: an ordinary launch.
-// kAfterInput: it reads what the launch before it writes, and waits for it
-// before its first load; its start-up is hidden.  kAfterNothing: it reads what an
-// earlier one wrote, which had ended when the launch before it allowed this one to
-// start (each allows it only after its own wait), so its tiles fill the SMs that
-// run out of work in the launch before; it waits for that one's end before its own,
-// so that the stream's order holds for what follows.
-enum After { kAfterAll = 0, kAfterInput = 1, kAfterNothing = 2 };
+// How a product follows the launch ahead of it (see launch_overlapped).  kAfterInput: it
+// waits for it before its first load; its start-up is hidden.  kAfterNothing: it reads
+// what an earlier one wrote, which had ended when the launch ahead allowed this one to
+// start, so its tiles fill the SMs that run out of work in the launch ahead; it
+// waits for that one's end before its own, so that the stream's order holds for
+// what follows.
+enum After { kAfterInput = 0, kAfterNothing = 1 };
 
 // CTAs of a tile (1, or a pair) and its columns; where everything lies in shared
 // memory, for an operand B that is MN-major or not and an epilogue.
@@ -566,22 +564,11 @@ cudaError_t launch_shape(const Gemm& g, int sm_count, cudaStream_t stream) {
   p.n_tiles = (p.cols + cols - 1) / cols;
   p.group = 8;  // 4 to 8 measured best: M=8192 H=I=2880 training step 1085 us against 1140 with all rows
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  cudaLaunchConfig_t cfg{};
-  const int64_t ctas = S::CG * S::SPLIT;  // of a cluster
-  cfg.gridDim = dim3(static_cast<unsigned>((S::SPLIT > 1 ? tiles : std::min<int64_t>(tiles, sm_count / S::CG)) * ctas));
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.after == kAfterAll ? 1 : 2;
+  const int ctas = S::CG * S::SPLIT;  // of a cluster
+  const int64_t clusters = S::SPLIT > 1 ? tiles : std::min<int64_t>(tiles, sm_count / S::CG);
   LaunchScope ls(g.name, stream);
-  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<S, AMN, BMN, EPI>, ta, tb, to[0], to[1], to[2], ti[0], ti[1], p);
+  return launch_overlapped(ffn_gemm_kernel<S, AMN, BMN, EPI>, static_cast<int>(clusters) * ctas, L::kThreads, L::kSmem, ctas,
+                           stream, ta, tb, to[0], to[1], to[2], ti[0], ti[1], p);
 }
 
 template <bool AMN, bool BMN, int EPI>
@@ -715,7 +702,6 @@ e4b_status e4b_gated_ffn_forward(const uint16_t* x, int64_t M, int64_t ldx, cons
   d.p.cols = H;
   d.p.K = I;
   d.p.err = g.p.err;
-  d.p.after = kAfterInput;
   if (cudaError_t err = launch_gemm<false, false, kEpiPlain>(d, di.sm_count, st); err != cudaSuccess)
     return cuda_fail(err, "ffn down launch");
   set_path("ffn.forward.tc");

@@ -160,6 +160,30 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   // rows o .. o + 7 and the up rows half + o .. half + o + 7 of a gated product.
   // Rows past the end read zeros, and are not written.
 
+  const unsigned char* lane_table = smem + lane * 4;
+  const Int4Bits bits = int4_bits();
+  if constexpr (FMT == kFmtCodebook) {
+    // Entry b: the pair of codes (b / 16, b % 16); thread b writes its 32 copies.
+    static_assert(kWarps * 32 == 256, "a thread per entry");
+    const float hi = p.book * codebook_entry(a.quant, threadIdx.x >> 4), lo = p.book * codebook_entry(a.quant, threadIdx.x & 15);
+    const uint32_t pair = pack_bf16x2(hi, lo);
+    const uint32_t rest = pack_bf16x2(hi - __uint_as_float(pair << 16), lo - __uint_as_float(pair & 0xffff0000u));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = (i + threadIdx.x) & 7;  // spread over the banks
+      reinterpret_cast<uint4*>(smem + threadIdx.x * 128)[q] = make_uint4(pair, pair, pair, pair);
+      if constexpr (TWO)
+        reinterpret_cast<uint4*>(smem + C::kTable + threadIdx.x * 128)[q] = make_uint4(rest, rest, rest, rest);
+    }
+    __syncthreads();
+  }
+
+  // x alone may come from the launch ahead (after_input), which has seen all before it end.
+  if (!a.after_input) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+
   // This warp's pieces, in order: every chunk of its share, tile after tile.
   // Lane l copies the 16-byte unit l % 8 of rows l / 8 + 4 i.
   int put_tile = cta, put_chunk = first, put_stage = 0, put_o = 0;
@@ -285,27 +309,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
       }
     }
   };
-  if (a.after_input) pdl_wait();
-  pdl_launch_dependents();
-  if (first < p.chunks) load_x(first);
-
-  const unsigned char* lane_table = smem + lane * 4;
-  const Int4Bits bits = int4_bits();
-  if constexpr (FMT == kFmtCodebook) {
-    // Entry b: the pair of codes (b / 16, b % 16); thread b writes its 32 copies.
-    static_assert(kWarps * 32 == 256, "a thread per entry");
-    const float hi = p.book * codebook_entry(a.quant, threadIdx.x >> 4), lo = p.book * codebook_entry(a.quant, threadIdx.x & 15);
-    const uint32_t pair = pack_bf16x2(hi, lo);
-    const uint32_t rest = pack_bf16x2(hi - __uint_as_float(pair << 16), lo - __uint_as_float(pair & 0xffff0000u));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = (i + threadIdx.x) & 7;  // spread over the banks
-      reinterpret_cast<uint4*>(smem + threadIdx.x * 128)[q] = make_uint4(pair, pair, pair, pair);
-      if constexpr (TWO)
-        reinterpret_cast<uint4*>(smem + C::kTable + threadIdx.x * 128)[q] = make_uint4(rest, rest, rest, rest);
-    }
-    __syncthreads();
+  if (a.after_input) {
+    pdl_wait();
+    pdl_launch_dependents();
   }
+  if (first < p.chunks) load_x(first);
 
   int stage = 0, buf = 0;
   const uint32_t piece_lane = g * 128 + (FMT == kFmtBf16 ? 0 : t * 4);
@@ -449,21 +457,8 @@ cudaError_t launch_one(const Params& p, int grid, cudaStream_t stream) {
   constexpr size_t smem = Cfg<FMT, GB, NT, RT, TWO>::kSmem;
   const void* f = reinterpret_cast<const void*>(gemv_kernel<FMT, GB, NT, RT, TWO>);
   if (cudaError_t err = ensure_smem_limit(f, smem); err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.a.after_input ? 2 : 1;
   LaunchScope ls(FMT == kFmtBf16 ? "gemv.bf16" : FMT == kFmtInt4 ? "gemv.int4" : "gemv.codebook", stream);
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<FMT, GB, NT, RT, TWO>, p);
+  return launch_overlapped(gemv_kernel<FMT, GB, NT, RT, TWO>, grid, kWarps * 32, smem, p.split, stream, p);
 }
 
 template <int FMT, int GB, bool TWO>

@@ -155,3 +155,51 @@ def test_training():
             "gate_up": f["dgate_up"], "down": f["ddown"]}
     for k, v in want.items():
         assert_close_layer(_np(got[k]), v, "gradient of " + k)
+
+
+def test_the_streams_order_holds():
+    """A chain of calls that each read what the last one wrote, with kernels and memsets of others between,
+    gives the same bits as the same chain with the device waited for after every call; captured as well."""
+    require_gpu()
+    M, H, I = 24, 512, 264
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    norm = e4b.BlockNorm(H, rand(H).to(BF), rand(H).to(BF), 1e-6, 0.5)
+    fn = e4b.GatedFFN((0.05 * rand(2 * I, H)).to(BF), (0.05 * rand(H, I)).to(BF))
+    square, _ = _int4(0.05 * rand(H, H), 32)
+    start = rand(M, H).to(BF)
+    ws = e4b.workspace(max(e4b.e4b_gated_ffn_forward_workspace_size(M, fn), e4b.e4b_gated_ffn_backward_workspace_size(M, fn),
+                           e4b.e4b_block_norm_backward_workspace_size(M, norm)))
+    b = {k: torch.empty(M, H, dtype=BF, device="cuda") for k in ("x", "n", "y", "dx", "dy", "q")}
+    pre, dgu, dd = _empty(M, 2 * I), _empty(2 * I, H), _empty(H, I)
+    dw = [torch.empty(H, device="cuda") for _ in range(2)]
+
+    def chain(wait):
+        b["x"].copy_(start)
+        b["y"].zero_()
+        for i in range(12):
+            e4b.e4b_block_norm_forward(b["x"], b["y"], None, norm, b["x"], b["n"])
+            wait()
+            e4b.e4b_gated_ffn_forward(b["n"], fn, b["y"], pre, ws)
+            wait()
+            e4b.workspace_clear_error(ws)  # a memset between two kernels
+            e4b.e4b_gemv_4bit(b["y"][:16], square, b["q"][:16])
+            wait()
+            b["y"][:16].add_(b["q"][:16])
+            e4b.e4b_gated_ffn_backward(b["n"], fn, pre, b["y"], b["dx"], dgu, dd, ws)
+            wait()
+            e4b.e4b_block_norm_backward(b["dx"], b["dx"], b["x"], b["y"], None, norm, b["dx"], b["dy"], None, *dw, ws)
+            wait()
+            b["x"].add_(b["dx"], alpha=1e-3).add_(dw[0].to(BF), alpha=1e-4).add_(dgu[:M], alpha=1e-3)
+        return [t.clone() for t in (*b.values(), pre, dgu, dd, *dw)]
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(chain(lambda: None), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(lambda: None)
+    for _ in range(2):
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
+    assert all(torch.isfinite(t.float()).all() for t in want)
