@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   using C = Cfg<FMT, GB, NT, RT, TWO>;
   constexpr int NB = C::kBlocks, NG = C::kGroups, KS = C::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ float red[2][kWarps][RT][NT][4][32];
+  __shared__ float4 red[2][kWarps][RT][NT][32];
   const GemvArgs& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int kw = p.kw, wk = warp % kw, wr = warp / kw;  // this warp's share of K, its row tiles of the CTA's
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
   // row's four keeps SPL of them and hands them over by shuffles, so that a
   // chunk's can be loaded while the one before it is multiplied.
   constexpr int SPL = NG > 4 ? NG / 4 : 1;
-  float ns[RT][2][SPL];
+  uint32_t ns[RT][2][SPL];  // as loaded: converted by their own chunk, which alone waits for them
   uint32_t nz[RT][2][SPL] = {};
   int64_t s_row[RT][2];
   auto scale_rows = [&](int tile) {
@@ -256,12 +256,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int64_t at = s_row[j][h] + (in ? grp : 0);
-            float v = a.scale_f32 ? static_cast<const float*>(a.scales)[at]
-                                  : bf16_bits_to_float(static_cast<const uint16_t*>(a.scales)[at]);
-            if constexpr (FMT == kFmtCodebook) v *= p.over_book;
-            ns[j][h][i] = in ? v : 0.0f;
+            ns[j][h][i] = 0;
+            if (in) ns[j][h][i] = a.scale_f32 ? static_cast<const uint32_t*>(a.scales)[at] : static_cast<const uint16_t*>(a.scales)[at];
             if constexpr (FMT == kFmtInt4)
-              if (a.zeros) nz[j][h][i] = a.zeros[at] & 15u;
+              if (a.zeros) nz[j][h][i] = a.zeros[at];
           }
       }
     }
@@ -329,8 +327,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < SPL; ++i) {
-            sc[j][h][i] = ns[j][h][i];
-            zz[j][h][i] = nz[j][h][i];
+            sc[j][h][i] = __uint_as_float(a.scale_f32 ? ns[j][h][i] : ns[j][h][i] << 16);
+            if constexpr (FMT == kFmtCodebook) sc[j][h][i] *= p.over_book;
+            zz[j][h][i] = nz[j][h][i] & 15u;
           }
       if (chunk + stride < p.chunks) {
         load_scales(chunk + stride);
@@ -412,39 +411,37 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
     for (int j = 0; j < RT; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[buf][warp][j][n][i][lane] = acc[j][n][i];
+        red[buf][warp][j][n][lane] = make_float4(acc[j][n][0], acc[j][n][1], acc[j][n][2], acc[j][n][3]);
     if (p.split > 1)
       cg::this_cluster().sync();
     else
       __syncthreads();
     if (rank == 0) {
-      const int count = tile_out * a.M;
-      for (int i = threadIdx.x; i < count; i += kWarps * 32) {
-        const int o = i % tile_out, m = i / tile_out;
-        const int col = tile * tile_out + o;
-        if (col >= nout) continue;
-        const int w0 = (o / warp_out) * kw, j = (o % warp_out) / rows_out, r = o % rows_out;
-        // MMA result i of lane (g, t): row g + 8 (i / 2), token 2 t + i % 2
-        auto total = [&](int row) {
-          float s = 0.0f;
-          for (int q = 0; q < p.split; ++q) {
-            const float* from = &red[buf][w0][j][m >> 3][((row >> 3) << 1) | (m & 1)][((row & 7) << 2) | ((m & 7) >> 1)];
-            if (q) from = cg::this_cluster().map_shared_rank(from, cg::this_cluster().block_rank() + q);
-            for (int w = 0; w < kw; ++w) s += from[w * RT * NT * 4 * 32];
+      // A warp adds up a row tile.  Lane (g, t) has rows g and g + 8, tokens 2 t and 2 t + 1.
+      for (int task = warp; task < (kWarps / kw) * RT * NT; task += kWarps) {
+        const int n = task % NT, j = task / NT % RT, r = task / NT / RT;
+        float c[4] = {};
+        for (int q = 0; q < p.split; ++q) {
+          const float4* from = &red[buf][r * kw][j][n][lane];
+          if (q) from = cg::this_cluster().map_shared_rank(from, cg::this_cluster().block_rank() + q);
+#pragma unroll 4
+          for (int w = 0; w < kw; ++w) {
+            const float4 v = from[w * RT * NT * 32];
+            c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
           }
-          return s;
-        };
-        float y = total(r);
-        if (glu) {
-          const float up = total(r + 8);
-          y = (a.epi == kGemvSilu ? silu_f32(y) : gelu_tanh_f32(y)) * up;
         }
-        const int64_t at = m * a.ldo + col;
-        if (a.out_f32)
-          static_cast<float*>(a.out)[at] = y;
-        else
-          static_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = n * 8 + 2 * t + (i & 1), col = tile * tile_out + r * warp_out + j * rows_out + g + (i >> 1) * 8;
+          if (m >= a.M || (glu && i > 1)) continue;
+          const float y = glu ? (a.epi == kGemvSilu ? silu_f32(c[i]) : gelu_tanh_f32(c[i])) * c[i | 2] : c[i];
+          if (col >= nout) continue;
+          const int64_t at = m * a.ldo + col;
+          if (a.out_f32)
+            static_cast<float*>(a.out)[at] = y;
+          else
+            static_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(y);
+        }
       }
     }
     if (p.split > 1) cg::this_cluster().sync();  // a CTA's sums stay until they are read
