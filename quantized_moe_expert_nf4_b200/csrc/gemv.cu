@@ -20,8 +20,8 @@
 // exchanged by row, so that those reads touch every bank once.
 //
 // Codes become exact bf16 values: int4 by or-ing the code into the mantissa of
-// 128 and subtracting 128 + zero, both exact; codebook entries by byte permutes over their bf16
-// bytes.  Products and group sums are fp32 in the MMA, the scales
+// 128 and subtracting 128 + zero, both exact; codebook entries by a table of byte pairs in
+// shared memory.  Products and group sums are fp32 in the MMA, the scales
 // multiply the group sums in fp32.  A codebook is taken times a factor, and the scales
 // over it, at which its entries fall nearer to bf16 values: 6 for FP4 (e2m1 values,
 // exact), 1.43672 for NF4 (of all factors the one with the least error over the codes
@@ -29,6 +29,22 @@
 // 1.36e-3, and 1.7e-3 of an entry at most instead of 3.1e-3).  With fp32 output an NF4
 // entry is the sum of two bf16 values (2^-17 of it at most); with bf16 output the
 // first alone, whose rounding stays below the output's.
+//
+// Measured on the device (graph replays, three sets of tensors in turn; the last
+// call's leave L2 in between, the others' stay):
+//   1 x 2048 x 2048 int4, blocks of 32, zero points    3.4 us (0.4 at the copy bandwidth)
+//   1 x 2880 x 5760 NF4, SwiGLU                        6.7 us (1.4): the tables' build, then
+//                                                      two or three chunks a warp
+//   13 x 2880 x 16411 FP4, blocks of 32               19.1 us (4.1)
+//   8 x 4096 x 32768 int4, blocks of 128, fp32 out    23.5 us (10.7): 3.0 TB/s
+// The large ones are bound by instruction issue with four warps a scheduler: the codes
+// alone take 32 (int4) to 59 (table) cycles for 16 rows x 32 k and scheduler, a half again for addresses,
+// scales and sums.  A copy of the kernel without 7 of 8 products took 15.5 us for the
+// last call, one without the copies 22.8.  Measured and not kept for it: x in shared
+// memory and 16 to 32 warps (26.6), a warp for the sums alone (39), all of K
+// by one warp (31.9: 128-byte pieces of 2 KB rows use DRAM pages badly), x read
+// again by every block (35), (chunk, row tile) items in equal runs with all sums
+// in shared memory (25.7).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -90,9 +106,10 @@ __device__ __forceinline__ uint32_t swz(int row) { return ((row & 1) << 2) | ((r
 // element order, one table lookup per byte.  The table holds each byte's pair once
 // per lane (entry b of lane l at byte 128 b + 4 l), so lookups never share a
 // bank; `lane_table` is the table's shared address + 4 l, its low 15 bits 4 l.
-// Two integer instructions and one shared load per pair measured 2x faster in
-// the mainloop than byte permutes over the codebook in registers (21 integer
-// instructions per word, on a pipe of half the issue rate).
+// Two integer instructions and one shared load per pair instead of byte permutes
+// over the codebook in registers (21 integer instructions per word, on a pipe of half
+// the issue rate): 13 x 2880 x 16411 FP4 21.2 us from 29.7, the scales' earlier
+// loads included.
 __device__ __forceinline__ void decode_table(uint32_t w, const unsigned char* lane_table, uint32_t v[4]) {
   v[0] = *reinterpret_cast<const uint32_t*>(lane_table + ((w << 7) & 0x7f80u));
   v[1] = *reinterpret_cast<const uint32_t*>(lane_table + ((w >> 1) & 0x7f80u));
@@ -483,8 +500,9 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   p.over_book = 1.0f / p.book;
   const int slots = 2 * di.sm_count;  // two CTAs fit an SM
   const int row_tiles = a.epi == kGemvNone ? (a.N + 15) / 16 : (a.N / 2 + 7) / 8;
-  // Two row tiles per warp share the tokens' registers; worth it once every warp
-  // of the GPU has several chunks anyway.
+  // Two row tiles per warp share the tokens' registers and a chunk's overhead; worth it
+  // once every warp of the GPU has several chunks anyway (8 x 4096 x 32768 int4 25 us
+  // against 30 with one; smaller products would leave SMs without rows).
   const int rt = a.M <= 8 && static_cast<int64_t>(row_tiles) * p.chunks >= 4ll * slots * kWarps ? 2 : 1;
   // The split of K over a CTA's warps that needs the fewest steps: chunks of a
   // warp's share, and about two for the sums that end a tile.
