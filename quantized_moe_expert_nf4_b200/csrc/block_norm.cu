@@ -29,15 +29,16 @@
 //   forward, 8192 x 2880, bf16 y, fp32 stream, bf16 n   45-50 us, 5.7 TB/s
 //   forward, 8192 x 2880, all bf16                      36 us, 5.2 TB/s
 //   forward, 8192 x 2049, all bf16 (shifted)            70 us, 1.9 TB/s
-//   backward, 8192 x 2880, bf16, fp32 dgate and dw      84.6 us, 3.35 TB/s
-//   backward, 2048 x 2049 (shifted)                     43.5 us, 1.55 TB/s
+//   backward, 8192 x 2880, bf16, fp32 dgate and dw      61.4 us, 4.6 TB/s
+//   backward, 2048 x 2049 (shifted)                     45 us, 1.5 TB/s
 //   forward of one row                                  2.6 us on the device, 9.5 with the call
-// The forward is bound by HBM.  The backward is bound by issue: five sums a row in two rounds
-// of barriers and about four times the arithmetic, at 24 warps an SM (registers hold a
-// thread's columns of three weight gradients).  What carried it: rows ahead in a ring 265
-// -> 132 us, packed fp32 -> 104, kernels with the usual inputs and outputs known at compile
-// time -> 85.  A row's weights in registers took the forward from 61 us to 45; two or four groups of
-// columns a thread where one is enough measured slower in both.
+// The forward is bound by HBM.  The backward is bound by issue and by HBM about alike at 24
+// warps an SM (registers hold a thread's columns of the weights and their gradients).  What
+// carried it: rows ahead in a ring 265 -> 132 us, packed fp32 -> 104, kernels with the usual
+// inputs and outputs known at compile time -> 85, weights in registers and what is the same
+// in every row taken out of the sums over rows -> 61.  A row's sums meet once: the sum
+// of k * yhat is taken term by term of d.  A row's weights in registers took the forward from 61 us to
+// 45; two or four groups of columns a thread where one is enough measured slower in both.
 #include <algorithm>
 #include <string>
 

@@ -483,11 +483,11 @@ struct Rows {
   }
 };
 
-// Sums of one to three values over the CTA's T threads (a multiple of 32, at most
+// Sums of one, two, three or six values over the CTA's T threads (a multiple of 32, at most
 // 512), to every thread.  Several values share the shuffles: a warp's halves (or
-// quarters) first exchange the values that each will add up (11 shuffles for two
-// and 12 for three instead of 18 and 27).  One barrier above one warp: a caller
-// that sums again passes another buffer of 64 floats.
+// quarters, eighths) first exchange the values that each will add up (11 shuffles
+// for two, 12 for three and 16 for six instead of 18, 27 and 54).  One barrier above one warp:
+// a caller that sums again passes another buffer of 64 floats (128 for six).
 __device__ __forceinline__ float add_xor(float v, int o) { return v + __shfl_xor_sync(0xffffffffu, v, o); }
 
 template <int NV>
@@ -517,6 +517,30 @@ __device__ __forceinline__ void row_sum(float v[NV], int T, float* red) {
     }
     v[0] = __shfl_sync(0xffffffffu, s, 0);
     v[1] = __shfl_sync(0xffffffffu, s, 16);
+  } else if constexpr (NV == 6) {
+    // lanes 4 i .. 4 i + 3 add up value 0, 1, 2, none, 3, 4, 5, none
+    const bool up = lane & 16, mid = lane & 8, odd = lane & 4;
+    float t[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) t[i] = (up ? v[i + 3] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 3], 16);
+    const float t0 = (mid ? t[2] : t[0]) + __shfl_xor_sync(0xffffffffu, mid ? t[0] : t[2], 8);
+    const float t1 = (mid ? 0.0f : t[1]) + __shfl_xor_sync(0xffffffffu, mid ? t[1] : 0.0f, 8);
+    float s = (odd ? t1 : t0) + __shfl_xor_sync(0xffffffffu, odd ? t0 : t1, 4);
+    s = add_xor(add_xor(s, 2), 1);
+    if (T > 32) {
+      const int place = (lane >> 2) * 16;
+      if ((lane & 3) == 0) red[place + warp] = s;
+      __syncthreads();
+      s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int w = (lane & 3) + 4 * j;
+        s += w < warps ? red[place + w] : 0.0f;
+      }
+      s = add_xor(add_xor(s, 2), 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, s, 4 * (i + i / 3));
   } else {
     // lanes 8 i .. 8 i + 7 add up value i (the fourth is none)
     const bool up = lane & 16, odd = lane & 8;

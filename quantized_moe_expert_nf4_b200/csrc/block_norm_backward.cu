@@ -111,7 +111,7 @@ template <class XT, class YT, int VPT, class COLS, bool ALL>
 __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     block_norm_backward_vec_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float red[2][2][64];  // as above
+  __shared__ float red[2][128];  // by turns, a row's sums
   const int T = blockDim.x;
   const COLS c(T, threadIdx.x, a.H);
   const bool has_y = ALL || a.y.p, next = ALL || a.w_next, post = ALL || a.w_post;
@@ -163,9 +163,24 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
   pdl_launch_dependents();
   for (int i = 0; i + 1 < stages; ++i) put();
   const F2 offset = f2(a.offset);
-  F8 s_post[VPT], s_next[VPT], s_gate[VPT];
+  // Sums over rows of dn * rhat, and of d * yhat times a row's or an element's f: dw_post
+  // and a channel gate's gradient are that times what is the same in every row.
+  F8 s_next[VPT], s_post[VPT];
+  auto channel = [&](int v) {  // f of a channel gate
+    const F8 f = kind == E4B_GATE_CHANNEL ? c.vector(a.vec_gate, a.gate_f32, v) : fill8(1.0f);
+    return a.sigmoid && kind == E4B_GATE_CHANNEL ? sigmoid8(f) : f;
+  };
+  auto w_post = [&](int v) { return post ? c.vector(a.w_post, a.w_f32, v) + offset : fill8(1.0f); };
+  auto w_next = [&](int v) { return c.vector(a.w_next, a.w_f32, v) + offset; };
+  // w_post and the channel's f, and w_next: in registers where a thread has one group.
+  constexpr bool kHeld = VPT == 1;
+  F8 held_y = fill8(1.0f), held_n = zero8();
+  if constexpr (kHeld) {
+    held_y = w_post(0) * channel(0);
+    if (next) held_n = w_next(0);
+  }
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) s_post[v] = s_next[v] = s_gate[v] = zero8();
+  for (int v = 0; v < VPT; ++v) s_post[v] = s_next[v] = zero8();
   auto flush = [&](int set, int64_t m, unsigned char* dx_row, unsigned char* dy_row) {
     if constexpr (COLS::kShared) {
       const unsigned char* out = ring + a.out_off + set * a.out_bytes;
@@ -202,29 +217,57 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
     auto load_dn = [&](int v) {
       return a.n_f32 ? c.template staged<float>(cur, a.dn, m, v) : c.template staged<uint16_t>(cur, a.dn, m, v);
     };
-    float s1[3] = {0.0f, 0.0f, 0.0f};  // sums of r^2, h * r, y^2
+    auto full = [&](int v) {  // f of a gate that has one for every element
+      const F8 f = a.gate_f32 ? c.template staged<float>(cur, a.gate, m, v) : c.template staged<uint16_t>(cur, a.gate, m, v);
+      return a.sigmoid ? sigmoid8(f) : f;
+    };
+    auto weight = [&](int v) { return kHeld ? held_y : w_post(v) * channel(v); };
+    // The sum of d * e, e = f * (w_post + offset) * y, which the post norm's and a token's
+    // gradient need, is taken term by term of d, so that one round of sums does for a row.
+    const bool along = has_y && (post || kind == E4B_GATE_TOKEN);
+    float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // of r^2, h * r, y^2; e * dr, e * h, e * r
+    auto add = [&](float& to, F2 q, int v) { to += c.in[v] ? lo(q) + hi(q) : 0.0f; };
     F8 h[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const F2 z = f2(0.0f);
+      F8 e = zero8();
       if (has_y) {
         const F8 y = c.template staged<YT>(cur, a.y, m, v);
-        const F2 q = dot8(y, y, z);
-        s1[2] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+        add(s[2], dot8(y, y, z), v);
+        if (along) {
+          e = y * weight(v);
+          if (kind == E4B_GATE_FULL) e = e * full(v);
+          if (has_dr) add(s[3], dot8(e, c.template staged<XT>(cur, a.dr, m, v), z), v);
+        }
       }
       if (next) {
         const F8 r = c.template staged<XT>(cur, a.x, m, v);
-        h[v] = load_dn(v) * (c.vector(a.w_next, a.w_f32, v) + offset);
-        const F2 q = dot8(r, r, z), u = dot8(h[v], r, z);
-        s1[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
-        s1[1] += c.in[v] ? lo(u) + hi(u) : 0.0f;
+        h[v] = load_dn(v) * (kHeld ? held_n : w_next(v));
+        add(s[0], dot8(r, r, z), v);
+        add(s[1], dot8(h[v], r, z), v);
+        if (along) {
+          add(s[4], dot8(e, h[v], z), v);
+          add(s[5], dot8(e, r, z), v);
+        }
       }
     }
-    row_sum<3>(s1, T, red[odd][0]);
-    const float rstd_r = rsqrtf(s1[0] * a.inv_h + a.eps), rstd_y = post ? rsqrtf(s1[2] * a.inv_h + a.eps) : 1.0f;
-    const float mean_r = s1[1] * rstd_r * a.inv_h;  // mean(h * rhat)
-    F8 k[VPT];
-    float s2[2] = {0.0f, 0.0f};  // sums of k * yhat, d * z * slope
+    row_sum<6>(s, T, red[odd]);
+    const float rstd_r = rsqrtf(s[0] * a.inv_h + a.eps), rstd_y = post ? rsqrtf(s[2] * a.inv_h + a.eps) : 1.0f;
+    const float mean_r = s[1] * rstd_r * a.inv_h;  // mean(h * rhat)
+    // scale * sum of d * e / f * rstd_y, f of a token's gate
+    const float de = a.scale * rstd_y * (next ? s[3] + rstd_r * (s[4] - rstd_r * mean_r * s[5]) : s[3]);
+    float f_token = 1.0f;
+    if (kind == E4B_GATE_TOKEN) {
+      f_token = load1(a.vec_gate, m, a.gate_f32);
+      float slope = 1.0f;
+      if (a.sigmoid) {
+        f_token = sigmoid_f32(f_token);
+        slope = f_token * (1.0f - f_token);
+      }
+      if (a.dgate && threadIdx.x == 0) store1(a.dgate, m, a.gate_f32, de * slope);
+    }
+    const float mean_y = post ? de * f_token * a.inv_h : 0.0f;  // mean(k * yhat)
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       F8 d = has_dr ? c.template staged<XT>(cur, a.dr, m, v) : zero8();
@@ -236,26 +279,15 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
       if (has_dx) c.template store<XT>(dx_p, dx_s, v, d);
       if (!has_y) continue;
       const F8 hat = c.template staged<YT>(cur, a.y, m, v) * f2(rstd_y);
-      const F8 w = post ? c.vector(a.w_post, a.w_f32, v) + offset : fill8(1.0f);
-      F8 dz = d * f2(a.scale);
-      if (kind != E4B_GATE_NONE) {
-        F8 f = kind == E4B_GATE_CHANNEL ? c.vector(a.vec_gate, a.gate_f32, v)
-               : kind == E4B_GATE_TOKEN ? fill8(load1(a.vec_gate, m, a.gate_f32))
-               : a.gate_f32             ? c.template staged<float>(cur, a.gate, m, v)
-                                        : c.template staged<uint16_t>(cur, a.gate, m, v);
-        F8 dg = dz * (hat * w);
-        if (a.sigmoid) {
-          f = sigmoid8(f);
-          dg = dg * (f * fma8(f, f2(-1.0f), fill8(1.0f)));
-        }
-        dz = dz * f;
-        if (kind == E4B_GATE_CHANNEL) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s_gate[v].p[j] = s_gate[v].p[j] + dg.p[j];
-        } else if (kind == E4B_GATE_TOKEN) {
-          const F2 q = (dg.p[0] + dg.p[1]) + (dg.p[2] + dg.p[3]);
-          s2[1] += c.in[v] ? lo(q) + hi(q) : 0.0f;
-        } else if (a.dgate) {
+      const F8 w = weight(v);
+      F8 df = d;  // times a row's or an element's f
+      if (kind == E4B_GATE_TOKEN) df = d * f2(f_token);
+      if (kind == E4B_GATE_FULL) {
+        const F8 f = full(v);
+        df = d * f;
+        if (a.dgate) {
+          F8 dg = d * (hat * w) * f2(a.scale);
+          if (a.sigmoid) dg = dg * (f * fma8(f, f2(-1.0f), fill8(1.0f)));
           unsigned char* row = static_cast<unsigned char*>(a.dgate) + m * a.gate.row;
           if (a.gate_f32)
             c.template store<float>(row, dg_s, v, dg);
@@ -263,19 +295,9 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
             c.template store<uint16_t>(row, dg_s, v, dg);
         }
       }
-      s_post[v] = fma8(dz, hat, s_post[v]);
-      k[v] = dz * w;
-      const F2 q = dot8(k[v], hat, f2(0.0f));
-      s2[0] += c.in[v] ? lo(q) + hi(q) : 0.0f;
+      s_post[v] = fma8(df, hat, s_post[v]);
+      if (has_dy) c.template store<YT>(dy_p, dy_s, v, fma8(hat, f2(-mean_y), df * w * f2(a.scale)) * f2(rstd_y));
     }
-    if (!has_y) continue;
-    if (post || kind == E4B_GATE_TOKEN) row_sum<2>(s2, T, red[odd][1]);
-    if (kind == E4B_GATE_TOKEN && a.dgate && threadIdx.x == 0) store1(a.dgate, m, a.gate_f32, s2[1]);
-    if (!has_dy) continue;
-    const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-      c.template store<YT>(dy_p, dy_s, v, fma8(c.template staged<YT>(cur, a.y, m, v), f2(-mean_y), k[v]) * f2(rstd_y));
   }
   if constexpr (COLS::kShared) {
     __syncthreads();
@@ -285,9 +307,11 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
   float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.H;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    if (post) c.sums(part, v, s_post[v]);
+    const F8 f = channel(v), all = s_post[v] * f2(a.scale);
+    if (post) c.sums(part, v, all * f);
     if (next) c.sums(part + plane, v, s_next[v]);
-    if (kind == E4B_GATE_CHANNEL) c.sums(part + 2 * plane, v, s_gate[v]);
+    if (kind == E4B_GATE_CHANNEL)
+      c.sums(part + 2 * plane, v, all * w_post(v) * (a.sigmoid ? f * fma8(f, f2(-1.0f), fill8(1.0f)) : fill8(1.0f)));
   }
 }
 

@@ -143,3 +143,9 @@ def test_gated_ffn_workspaces(lib):
     assert lib.e4b_gated_ffn_forward_workspace_size(0, ctypes.byref(f)) == 0
     assert lib.e4b_gated_ffn_forward_workspace_size(3, ctypes.byref(f)) == 256 + (3 * 1000 * 2 + 255) // 256 * 256
     assert lib.e4b_gated_ffn_backward_workspace_size(3, ctypes.byref(f)) >= 256 + 3 * 3 * 1000 * 2
+
+
+def test_int4_is_the_dense_products_alone(lib):
+    """The expert stacks know no zero points: their calls refuse the type."""
+    assert lib.e4b_quantize_stack(P, 0, 1, 64, 64, 64, e4b.E4B_QUANT_INT4, P, P, None) == 1
+    assert "quant_type" in lib.e4b_last_error().decode()

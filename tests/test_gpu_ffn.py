@@ -206,3 +206,27 @@ def test_same_bits_every_time_on_streams_and_in_graphs(M):
     grads = _backward(x, fn, pre2, dout)
     assert torch.equal(pre, pre2) and torch.equal(out, again)
     assert all(torch.equal(t, grads[k]) for t, k in zip(g, ("dx", "dgate_up", "ddown")))
+
+
+def test_offsets_past_32_bits():
+    """Pre-activations of more than 2^31 elements: the last rows of a long input are those of a short one."""
+    require_gpu()
+    M, H, I, last = 400_000, 64, 2880, 256
+    x, wgu, wd, dout = _inputs(last, H, I)
+    fn = e4b.GatedFFN(wgu, wd)
+    pre = torch.empty(last, 2 * I, dtype=BF, device="cuda")
+    out = _forward(x, fn, pre)
+    g = _backward(x, fn, pre, dout, ("dx",))
+    long_x, long_dout = (torch.cat([torch.zeros(M - last, H, dtype=BF, device="cuda"), t]) for t in (x, dout))
+    long_pre = torch.empty(M, 2 * I, dtype=BF, device="cuda")
+    long_out = _forward(long_x, fn, long_pre)
+    long_g = _backward(long_x, fn, long_pre, long_dout)
+    assert not long_out[:-last].any() and not long_pre[:-last].any() and not long_g["dx"][:-last].any()
+    # Sums of the same products, in tiles of another size: differences in the last bits of
+    # 32 (and through them a bf16 step of h and of dpre).
+    def near(got, want):
+        return torch.linalg.vector_norm(got.double() - want.double()) <= 2.0 ** -8 * torch.linalg.vector_norm(want.double())
+
+    assert near(long_out[-last:], out) and near(long_pre[-last:], pre) and near(long_g["dx"][-last:], g["dx"])
+    short = _backward(x, fn, pre, dout)
+    assert near(long_g["dgate_up"], short["dgate_up"]) and near(long_g["ddown"], short["ddown"])
