@@ -44,7 +44,7 @@
 // memory and 16 to 32 warps (26.6), a warp for the sums alone (39), all of K
 // by one warp (31.9: 128-byte pieces of 2 KB rows use DRAM pages badly), x read
 // again by every block (35), (chunk, row tile) items in equal runs with all sums
-// in shared memory (25.7).
+// in shared memory (25.7), rows shared out evenly to the last row tile (24.0).
 #include <cooperative_groups.h>
 
 #include <algorithm>
