@@ -417,7 +417,7 @@ e4b_status check_norm(const e4b_block_norm* p, int64_t M, const void* y, const v
     return fail(E4B_ERR_INVALID_ARGUMENT, "gate_dtype must be F32 or BF16 and gate aligned to its elements");
   if (!y && M > 0 && (kind != E4B_GATE_NONE || p->w_post))
     return fail(E4B_ERR_INVALID_ARGUMENT, "a gate or w_post needs the block's output y");
-  if (!y && !p->w_next) return fail(E4B_ERR_INVALID_ARGUMENT, "nothing to compute: neither y nor w_next");
+  if (!y && !p->w_next && M > 0) return fail(E4B_ERR_INVALID_ARGUMENT, "nothing to compute: neither y nor w_next");
   return E4B_OK;
 }
 

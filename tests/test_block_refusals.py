@@ -69,6 +69,20 @@ def test_block_norm_backward(lib, norm, args, status, word):
     assert st == status and word in msg, msg
 
 
+@pytest.mark.parametrize("post,nxt", [(True, True), (True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("kind", [0, 1, 2, 3])
+def test_block_norm_takes_no_rows(lib, post, nxt, kind):
+    """A tensor without rows has no address: whatever the block has, its arguments are in order (what may be
+    refused is the device).  No output is asked for, so nothing is launched where there is a device."""
+    norm = _norm(w_post=P if post else None, w_next=P if nxt else None)
+    gate = P if kind == 1 else None
+    st, msg = _norm_forward(lib, norm, x=None, y=None, r=None, n=None, gate=gate, kind=kind, M=0)
+    assert st in (0, 2, 4), msg
+    st, msg = _norm_backward(lib, norm, dr=None, dn=None, r=None, y=None, gate=gate, kind=kind, M=0, dx=None, dy=None,
+                             dwp=None, dwn=None, ws=None, nbytes=0)
+    assert st in (0, 2, 4), msg
+
+
 def test_block_norm_workspace(lib):
     size = lambda M, H: lib.e4b_block_norm_backward_workspace_size(M, ctypes.byref(_norm(H=H)))  # noqa: E731
     assert size(0, 64) == 0 and size(4, 0) == 0 and size(4, 16385) == 0

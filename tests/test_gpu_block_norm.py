@@ -246,6 +246,19 @@ def test_no_rows():
     assert e4b.last_path() == "block_norm.backward.empty"
 
 
+@pytest.mark.parametrize("post,nxt", [(True, True), (True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+def test_no_rows_of_any_block(post, nxt, gate):
+    """Sums over no rows are zero, whichever of the norms the block has."""
+    require_gpu()
+    t, norm, _ = _inputs(0, 72, gate, post=post, nxt=nxt)
+    _forward(t, norm)
+    out = _backward(t, norm)
+    sums = ("dw_post", "dw_next") + (("dgate",) if gate == "channel" else ())
+    assert all(torch.all(out[k] == 0) for k in sums if out[k] is not None)
+    assert e4b.last_path() == "block_norm.backward.empty"
+
+
 def test_same_bits_every_time_on_streams_and_in_graphs():
     require_gpu()
     t, norm, _ = _inputs(3000, 520, "channel")
