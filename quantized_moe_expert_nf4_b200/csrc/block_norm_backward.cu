@@ -89,9 +89,9 @@ __global__ void __launch_bounds__(T, VPT == 1 ? 768 / T : 1)
     const float mean_y = post ? s2[0] * a.inv_h * rstd_y : 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const F8 y = rows.template load<YT>(a.y, m, v);
-      c.store(reinterpret_cast<YT*>(static_cast<unsigned char*>(a.dy.p) + m * a.dy.row), v,
-              fma8(y, f2(-mean_y), k[v]) * f2(rstd_y));
+      F8 dy = k[v];  // without its norm dy does not depend on y, which may be infinite
+      if (post) dy = fma8(rows.template load<YT>(a.y, m, v), f2(-mean_y), dy) * f2(rstd_y);
+      c.store(reinterpret_cast<YT*>(static_cast<unsigned char*>(a.dy.p) + m * a.dy.row), v, dy);
     }
   }
   const int64_t plane = static_cast<int64_t>(a.parts) * a.H;
@@ -296,7 +296,11 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 1 ? 2 : 1)
         }
       }
       s_post[v] = fma8(df, hat, s_post[v]);
-      if (has_dy) c.template store<YT>(dy_p, dy_s, v, fma8(hat, f2(-mean_y), df * w * f2(a.scale)) * f2(rstd_y));
+      if (has_dy) {
+        F8 dy = df * w * f2(a.scale);
+        if (post) dy = fma8(hat, f2(-mean_y), dy) * f2(rstd_y);  // without its norm dy does not depend on y, which may be infinite
+        c.template store<YT>(dy_p, dy_s, v, dy);
+      }
     }
   }
   if constexpr (COLS::kShared) {

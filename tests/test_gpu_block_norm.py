@@ -192,6 +192,31 @@ def test_an_infinity_or_nan_stays_in_its_row():
         assert not torch.isfinite(r1[7, 3]) and torch.isnan(n1[7, 3])
 
 
+@pytest.mark.parametrize("H,base", [(96, 0), (131, 0), (96, 1), (2880, 0), (4104, 0), (8200, 0)])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+@pytest.mark.parametrize("nxt", [True, False])
+def test_an_infinite_block_output_without_its_norm(H, base, gate, nxt):
+    """Without w_post, dy = scale * f * d does not depend on y: an infinity or a NaN there stays out of dy and dx,
+    and reaches the gate's gradient at its own place only."""
+    require_gpu()
+    t, norm, ref = _inputs(9, H, gate, post=False, nxt=nxt)
+    if base:
+        buf = torch.zeros(9 * H + base, dtype=BF, device="cuda")
+        buf[base:].copy_(t["y"].reshape(-1))
+        t["y"] = buf[base:].view(9, H)
+    want = _backward(t, norm)
+    t["y"][2, 5], t["y"][4, H - 1], t["y"][6, 0] = float("inf"), float("-inf"), float("nan")
+    got = _backward(t, norm)
+    assert e4b.last_path().startswith("block_norm.backward")
+    assert torch.equal(got["dy"], want["dy"]) and torch.equal(got["dx"], want["dx"])
+    if nxt:
+        assert torch.equal(got["dw_next"], want["dw_next"])
+    if gate in ("channel", "full"):
+        touched = torch.isfinite(want["dgate"].float()) & ~torch.isfinite(got["dgate"].float())
+        at = ((5,), (H - 1,), (0,)) if gate == "channel" else ((2, 5), (4, H - 1), (6, 0))
+        assert int(touched.sum()) == 3 and all(touched[i] for i in at)
+
+
 def test_in_place():
     require_gpu()
     t, norm, _ = _inputs(300, 264, "full")
