@@ -131,12 +131,14 @@ __device__ __forceinline__ F8 unpack8(uint4 q) {
            f2(__uint_as_float(q.z << 16), __uint_as_float(q.z & 0xffff0000u)),
            f2(__uint_as_float(q.w << 16), __uint_as_float(q.w & 0xffff0000u))}};
 }
-// A 32-byte load (of data that no kernel writes meanwhile).
+// A 32-byte load.  Coherent, and kept behind pdl_wait(): the launch ahead may have written the
+// vector (a channel gate from a product) after this kernel's CTAs had started.
 __device__ __forceinline__ F8 load8(const float* p) {
   float v[8];
-  asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-      : "l"(p));
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p)
+               : "memory");
   return {{f2(v[0], v[1]), f2(v[2], v[3]), f2(v[4], v[5]), f2(v[6], v[7])}};
 }
 __device__ __forceinline__ F8 load8(const uint16_t* p) { return unpack8(*reinterpret_cast<const uint4*>(p)); }

@@ -203,3 +203,50 @@ def test_the_streams_order_holds():
         graph.replay()
         assert all(torch.equal(p, q) for p, q in zip(out, want))
     assert all(torch.isfinite(t.float()).all() for t in want)
+
+
+@pytest.mark.parametrize("H", [512, 2049, 4096, 8200])
+def test_vectors_written_by_the_call_ahead(H):
+    """fp32 weights and a channel gate that the call just ahead on the stream writes: the same bits as with the
+    device waited for in between, eager and captured."""
+    require_gpu()
+    M, K = 40, 4096
+    g = torch.Generator(device="cuda").manual_seed(H)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    source, _ = _int4(rand(H, K) / K ** 0.5, 32)
+    seeds, x, y = rand(6, 1, K).to(BF), rand(M, H).to(BF), rand(M, H).to(BF)
+    dr, dn = rand(M, H).to(BF), rand(M, H).to(BF)
+    vec = {k: torch.zeros(1, H, device="cuda") for k in ("w_post", "w_next", "gate")}
+    norm = e4b.BlockNorm(H, vec["w_post"].view(H), vec["w_next"].view(H), 1e-6, 0.5)
+    ws = e4b.workspace(e4b.e4b_block_norm_backward_workspace_size(M, norm))
+
+    def chain(wait):
+        outs = []
+        for t in vec.values():
+            t.zero_()
+        for i in range(12):
+            for j, name in enumerate(vec):  # the last written stands right ahead of its reader
+                e4b.e4b_gemv_4bit(seeds[(i + j) % 6], source, vec[name])
+                wait()
+                r, n, dx, dy = (torch.empty_like(x) for _ in range(4))
+                dw = [torch.empty(H, device="cuda") for _ in range(3)]
+                e4b.e4b_block_norm_forward(x, y, vec["gate"].view(H), norm, r, n)
+                wait()
+                e4b.e4b_gemv_4bit(seeds[(i + j + 3) % 6], source, vec[name])
+                wait()
+                e4b.e4b_block_norm_backward(dr, dn, r, y, vec["gate"].view(H), norm, dx, dy, *dw, ws)
+                wait()
+                outs += [r, n, dx, dy, *dw]
+        return outs
+
+    want = chain(torch.cuda.synchronize)
+    assert all(torch.isfinite(t.float()).all() for t in want)
+    assert not torch.equal(want[7 * 35], want[7 * 34])  # the gate written in between shows
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(chain(lambda: None), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(lambda: None)
+    for _ in range(2):
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
