@@ -84,6 +84,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// mbar_wait() by a whole warp: one answer for all of its lanes, of which one may run out
+// of time where another still sees the phase end, and the lanes together again, as
+// the .aligned instructions behind a wait ask.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
 // Shared-memory int with acquire / release ordering at CTA scope.
 __device__ __forceinline__ int ld_acquire_shared(const int* p) {
   int v;

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
       const int m0 = m_tile * (kTileM * CG) + rank * kTileM;
       for (int kb = kb_first; kb < kb_end; ++kb, ++it) {
         const int s = it % KS;
-        if (it >= KS && !mbar_wait(&empty[s], ((it / KS) - 1) & 1)) {
+        if (it >= KS && !mbar_wait_warp(&empty[s], ((it / KS) - 1) & 1)) {
           record_error(p.err, kErrWaitEmpty);
           ok = false;
           break;
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
     // The last stages: consumed (their barriers' last arrivals come from the
     // MMAs), or, after a wait that gave up, at least landed before the CTA ends.
     for (uint32_t j = it < KS ? 0 : it - KS; j < it; ++j) {
-      if (ok) ok = mbar_wait(&empty[j % KS], (j / KS) & 1);
-      if (!ok && rank == 0) mbar_wait(&full[j % KS], (j / KS) & 1);
+      if (ok) ok = mbar_wait_warp(&empty[j % KS], (j / KS) & 1);
+      if (!ok && rank == 0) mbar_wait_warp(&full[j % KS], (j / KS) & 1);
     }
     if constexpr (SPLIT > 1) cluster_sync_all();  // with the epilogue's
   } else if (warp == 1) {
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++j) {
         const uint32_t slot = j & 1;
-        if (j >= 2 && !mbar_wait(&acc_empty[slot], ((j >> 1) - 1) & 1)) {
+        if (j >= 2 && !mbar_wait_warp(&acc_empty[slot], ((j >> 1) - 1) & 1)) {
           record_error(p.err, kErrWaitEmpty);
           break;
         }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
         const uint32_t d = tmem + slot * BN;
         for (int kb = kb_first; kb < kb_end; ++kb, ++it) {
           const int s = it % KS;
-          if (!mbar_wait(&full[s], (it / KS) & 1)) {
+          if (!mbar_wait_warp(&full[s], (it / KS) & 1)) {
             record_error(p.err, kErrWaitFull);
             ok = false;
             break;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
           if (lane == 0) bulk_wait_group_read<0>();
           put_in(col0 + c_first, row0);
         }
-      if (!mbar_wait(&acc_full[slot], (j >> 1) & 1)) {
+      if (!mbar_wait_warp(&acc_full[slot], (j >> 1) & 1)) {
         record_error(p.err, kErrWaitFull);
         ok = false;
         if constexpr (SPLIT == 1) break;
@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
         const int col = col0 + c;
         if (row0 >= p.rows || col >= p.cols) break;
         float v[32];
+        __syncwarp();  // lane 0 has just set off the last columns' stores
         tmem_ld_32x32b_x32(acc + c, v);
         if constexpr (EPI == kEpiPlain) {
           unsigned char* piece = pieces + (piece_no++ % L::kPieces) * kPieceBytes;
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
           unsigned char* in = in_pieces + (in_get & 1) * 2 * kPieceBytes;
           if (lane == 0) bulk_wait_group_read<0>();  // the last stores, of h and of the other pair
           if (c + 32 < c_first + kCols && col + 32 < p.cols) put_in(col + 32, row0);
-          if (!mbar_wait(&in_bar[in_get & 1], (in_get >> 1) & 1)) {
+          if (!mbar_wait_warp(&in_bar[in_get & 1], (in_get >> 1) & 1)) {
             record_error(p.err, kErrWaitFull);
             ok = false;
             tmem_ld_wait();
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(Layout<S, BMN, EPI>::kThreads, 1)
       }
     }
     if constexpr (EPI == kEpiDglu)  // after a wait that gave up: loads in flight land first
-      for (; in_get < in_put; ++in_get) mbar_wait(&in_bar[in_get & 1], (in_get >> 1) & 1);
+      for (; in_get < in_put; ++in_get) mbar_wait_warp(&in_bar[in_get & 1], (in_get >> 1) & 1);
     if (lane == 0) bulk_wait_group_all();
   }
   if (p.after == kAfterNothing) pdl_wait();

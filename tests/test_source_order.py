@@ -58,3 +58,26 @@ def test_early_kernels_read_memory_in_order(path):
             continue
         assert ".nc" not in body, body
         assert qualifier == "volatile" and '"memory"' in body, body
+
+
+def _function(code, name):
+    at = re.search(r"\b" + name + r"\([^)]*\)\s*\{", code).end()
+    depth, i = 1, at
+    while depth:
+        depth += (code[i] == "{") - (code[i] == "}")
+        i += 1
+    return code[at:i - 1]
+
+
+def test_warps_meet_before_aligned_barriers():
+    """barrier.cluster with .aligned wants a warp's lanes together; its callers come from branches of single lanes."""
+    body = _function(_code(os.path.join(CSRC, "tcgen05.cuh")), "cluster_sync_all")
+    assert ".aligned" in body and 0 <= body.find("__syncwarp()") < body.find("barrier.cluster")
+
+
+def test_a_warp_leaves_a_wait_together():
+    """In the feed-forward kernel whole warps wait and go on to .aligned instructions: the wait's answer is one for
+    all lanes.  (A wait by itself answers each lane, and one may run out of time alone.)"""
+    code = _code(os.path.join(CSRC, "ffn.cu"))
+    assert not re.search(r"\bmbar_wait\(", code) and "mbar_wait_warp(" in code
+    assert "__all_sync" in _function(_code(os.path.join(CSRC, "async.cuh")), "mbar_wait_warp")
