@@ -135,6 +135,20 @@ def test_large_tiles(M, H, I):
     _check_backward(M, H, I)
 
 
+def test_pair_tiles_in_every_product():
+    """Sizes at which each of the six products takes 256 x 256 tiles: whole ones, and ragged ones at both edges."""
+    require_gpu()
+    _check_forward(2500, 2200, 2200, save=True)
+    _check_backward(2500, 2200, 2200, "gelu")
+
+
+@pytest.mark.parametrize("M,H,I", [(1, 2880, 2880), (8, 4104, 2888), (3, 2888, 4104), (1, 4096, 11008)], ids=lambda v: str(v))
+def test_a_few_rows_of_large_weights(M, H, I):
+    """A warp takes two row tiles of the weights, gated and plain."""
+    require_gpu()
+    _check_forward(M, H, I, "gelu" if M == 8 else "silu", pad=8 * (M % 2))
+
+
 def test_gradients_asked_for_one_by_one():
     require_gpu()
     x, wgu, wd, dout = _inputs(200, 320, 136)

@@ -95,6 +95,56 @@ def test_gated(N, K, M, out):
     _check(M, N, K, 32, "int4", zeros=True, out=out, swiglu=True, scale_dtype=BF)
 
 
+def _check_large(M, N, K, group, kind, zeros=False, scale_dtype=F32, out=BF, swiglu=False):
+    """_check() with the float64 products on the GPU: matrices at which a warp takes two row tiles."""
+    handle, w = _weight(N, K, group, kind, zeros, scale_dtype)
+    x, w = _x(M, K, 8), torch.from_numpy(w).cuda()
+    cols = N // 2 if swiglu else N
+    buf = torch.full((M, cols + 8), 7.0, dtype=out, device="cuda")
+    e4b.e4b_gemv_4bit(x, handle, buf[:, :cols], e4b.E4B_EPI_SWIGLU if swiglu else e4b.E4B_EPI_NONE)
+    assert torch.all(buf[:, cols:] == 7.0)
+    y, size = x.double() @ w.T, x.double().abs() @ w.abs().T
+    err = (2.0 ** -16 + (0.0 if kind != "nf4" else 2.0 ** -8 if out == BF else 2.0 ** -16)) * size
+    want = y
+    if swiglu:
+        a, b, ea, eb = y[:, :cols], y[:, cols:], err[:, :cols], err[:, cols:]
+        want = torch.nn.functional.silu(a) * b
+        err = 1.1 * ea * (b.abs() + eb) + torch.nn.functional.silu(a).abs() * eb + 2.0 ** -19 * want.abs()
+    off = (buf[:, :cols].double() - want).abs()
+    assert torch.all(off <= err + HALF[out] * (want.abs() + err))
+    assert off.norm() <= (3e-3 if out == BF else 2e-5) * (2 if swiglu else 1) * want.norm()
+
+
+# A warp takes two row tiles from 32 * 296 (row tile, chunk of 256 codes) pairs on, at up to 8 tokens.  Row counts
+# end inside a tile, and inside its second half; K ends inside a chunk, or not.
+@pytest.mark.parametrize("kind,group,zeros,scale_dtype", [
+    ("nf4", 32, False, BF), ("nf4", 64, False, F32), ("nf4", 128, False, BF), ("fp4", 32, False, F32), ("fp4", 64, False, BF),
+    ("fp4", 128, False, F32), ("int4", 32, True, BF), ("int4", 64, True, F32), ("int4", 128, True, BF), ("int4", 32, False, F32)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_two_row_tiles(kind, group, zeros, scale_dtype, out):
+    require_gpu()
+    M = 8 if (group == 64) == (out == BF) else 1
+    _check_large(M, 20011 if M == 1 else 20021, 2048 if group == 128 else 2080 if group == 32 else 2112, group, kind, zeros,
+                 scale_dtype, out)
+
+
+@pytest.mark.parametrize("kind,group,zeros,out,M", [("nf4", 64, False, BF, 1), ("nf4", 32, False, F32, 7), ("fp4", 128, False, BF, 8),
+                                                    ("int4", 32, True, BF, 8), ("int4", 64, False, F32, 1), ("int4", 128, True, BF, 3)])
+@pytest.mark.parametrize("half", [10010, 10021])
+def test_two_row_tiles_gated(kind, group, zeros, out, M, half):
+    require_gpu()
+    _check_large(M, 2 * half, 2048, group, kind, zeros, BF if zeros else F32, out, swiglu=True)
+
+
+@pytest.mark.parametrize("kind,group,zeros,out,M", [("nf4", 32, False, BF, 8), ("nf4", 64, False, F32, 2), ("fp4", 64, False, BF, 1),
+                                                    ("int4", 128, True, F32, 8), ("int4", 32, True, BF, 16)])
+@pytest.mark.parametrize("N,K", [(40011, 2048), (160021, 256), (22003, 96 * 64)], ids=lambda v: str(v))
+def test_several_tiles_a_cta(kind, group, zeros, out, M, N, K):
+    """More tiles than CTAs: a CTA goes on to rows with scales of their own and sums in its other buffer."""
+    require_gpu()
+    _check_large(M, N, K, group, kind, zeros, BF, out)
+
+
 def test_reads_a_quantised_stack():
     """One expert of e4b_quantize_stack is a matrix with groups of 64: same result as the grouped GEMM's oracle."""
     require_gpu()
