@@ -144,11 +144,14 @@ struct Cfg {
   static constexpr int kChunkK = kBlocks * 32;
   static constexpr int kGroups = FMT == kFmtBf16 ? 1 : kBlocks / GB;  // groups in a chunk
   static constexpr uint32_t kPiece = RT * 16 * 128;
-  // Pieces in flight per warp: 64 KB per CTA, less beside two tables.
+  // Pieces in flight per warp: 64 KB per CTA, 32 beside two tables.
   static constexpr int kStages = TWO ? 2 : 4 / RT;
   static constexpr uint32_t kTable = FMT == kFmtCodebook ? 256 * 128 : 0;
   static constexpr uint32_t kTables = kTable * (TWO ? 2 : 1);
   static constexpr uint32_t kSmem = kTables + kWarps * kStages * kPiece;
+  static constexpr uint32_t kSums = 2 * kWarps * RT * NT * 32 * 16;  // `red`
+  // launch_gemv() counts on two CTAs an SM (228 KB, of which each CTA costs 1 more).
+  static_assert(2 * (kSmem + kSums + 1024) <= 228 * 1024, "two CTAs fit an SM");
 };
 
 template <int FMT, int GB, int NT, int RT, bool TWO>
@@ -478,7 +481,9 @@ cudaError_t launch_one(const Params& p, int grid, cudaStream_t stream) {
 template <int FMT, int GB, bool TWO>
 cudaError_t launch_rows(const Params& p, int rt, int grid, cudaStream_t stream) {
   if (p.a.M > 8) return launch_one<FMT, GB, 2, 1, TWO>(p, grid, stream);
-  return rt == 2 ? launch_one<FMT, GB, 1, 2, TWO>(p, grid, stream) : launch_one<FMT, GB, 1, 1, TWO>(p, grid, stream);
+  if constexpr (!TWO)  // launch_gemv() asks for no two row tiles there
+    if (rt == 2) return launch_one<FMT, GB, 1, 2, TWO>(p, grid, stream);
+  return launch_one<FMT, GB, 1, 1, TWO>(p, grid, stream);
 }
 
 template <int FMT, bool TWO>
@@ -503,7 +508,10 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   // Two row tiles per warp share the tokens' registers and a chunk's overhead; worth it
   // once every warp of the GPU has several chunks anyway (8 x 4096 x 32768 int4 25 us
   // against 30 with one; smaller products would leave SMs without rows).
-  const int rt = a.M <= 8 && static_cast<int64_t>(row_tiles) * p.chunks >= 4ll * slots * kWarps ? 2 : 1;
+  // Not with two tables: their shared memory and two row tiles' leave an SM one CTA
+  // (8 x 4096 x 32768 NF4, blocks of 64, fp32 out 41.0 us against 45.9 with two row tiles).
+  const bool two = a.fmt == kGemvCodebook && a.out_f32 && a.quant != E4B_QUANT_FP4;
+  const int rt = a.M <= 8 && !two && static_cast<int64_t>(row_tiles) * p.chunks >= 4ll * slots * kWarps ? 2 : 1;
   // The split of K over a CTA's warps that needs the fewest steps: chunks of a
   // warp's share, and about two for the sums that end a tile.
   const int units = (row_tiles + rt - 1) / rt;
@@ -524,8 +532,7 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   const int grid = p.split > 1 ? p.tiles * p.split : std::min(p.tiles, slots);
   if (a.fmt == kGemvBf16) return launch_rows<kFmtBf16, 1, false>(p, rt, grid, stream);
   if (a.fmt == kGemvInt4) return launch_group<kFmtInt4, false>(p, rt, grid, stream);
-  return a.out_f32 && a.quant != E4B_QUANT_FP4 ? launch_group<kFmtCodebook, true>(p, rt, grid, stream)
-                   : launch_group<kFmtCodebook, false>(p, rt, grid, stream);
+  return two ? launch_group<kFmtCodebook, true>(p, rt, grid, stream) : launch_group<kFmtCodebook, false>(p, rt, grid, stream);
 }
 
 }  // namespace e4b
