@@ -514,7 +514,7 @@ typedef struct {
  * Requires K a multiple of the group; any N >= 1, even with SwiGLU;
  * 0 <= M <= 16 (longer inputs: e4b_grouped_4bit_gemm() with one group).
  * fp32 accumulation; scales multiply group sums in fp32.  INT4 and FP4 values
- * are exact; NF4 entries are within 1.8e-3 with bf16 output and 2^-17 with
+ * are exact; NF4 entries are within 1.8e-3 with bf16 output and 2^-18 with
  * fp32 output.  Deterministic.  No workspace.  out may not overlap x.
  */
 E4B_API e4b_status e4b_gemv_4bit(const uint16_t* x, int64_t M, int64_t ldx, const e4b_group_weight* w,

@@ -26,9 +26,10 @@
 // over it, at which its entries fall nearer to bf16 values: 6 for FP4 (e2m1 values,
 // exact), 1.43672 for NF4 (of all factors the one with the least error over the codes
 // of Gaussian weights in blocks of 64: 0.78e-3 of the weights' rms instead of
-// 1.36e-3, and 1.7e-3 of an entry at most instead of 3.1e-3).  With fp32 output an NF4
-// entry is the sum of two bf16 values (2^-17 of it at most); with bf16 output the
-// first alone, whose rounding stays below the output's.
+// 1.36e-3, and 1.7e-3 of an entry at most instead of 3.1e-3).  With bf16 output that
+// is all: the rounding stays below the output's.  With fp32 output an NF4 entry is the sum
+// of two bf16 values of one sign, times 1.4376 (of all factors the one with the least
+// error of such pairs: 2^-18.8 of an entry at most).
 //
 // Measured on the device (graph replays, three sets of tensors in turn; the last
 // call's leave L2 in between, the others' stay):
@@ -186,7 +187,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const __grid_const
     // Entry b: the pair of codes (b / 16, b % 16); thread b writes its 32 copies.
     static_assert(kWarps * 32 == 256, "a thread per entry");
     const float hi = p.book * codebook_entry(a.quant, threadIdx.x >> 4), lo = p.book * codebook_entry(a.quant, threadIdx.x & 15);
-    const uint32_t pair = pack_bf16x2(hi, lo);
+    // The first of two values is cut, not rounded: the second then has its sign, and an
+    // infinite x keeps its own (inf * first + inf * second).
+    const uint32_t pair = TWO ? __byte_perm(__float_as_uint(hi), __float_as_uint(lo), 0x7632u) : pack_bf16x2(hi, lo);
     const uint32_t rest = pack_bf16x2(hi - __uint_as_float(pair << 16), lo - __uint_as_float(pair & 0xffff0000u));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -501,7 +504,8 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   Params p{};
   p.a = a;
   p.chunks = static_cast<int>((a.row_bytes + 127) / 128);
-  p.book = a.quant == E4B_QUANT_FP4 ? 6.0f : 1.43672f;
+  const bool two = a.fmt == kGemvCodebook && a.out_f32 && a.quant != E4B_QUANT_FP4;  // NF4 entries as two bf16 values
+  p.book = a.quant == E4B_QUANT_FP4 ? 6.0f : two ? 1.4376f : 1.43672f;
   p.over_book = 1.0f / p.book;
   const int slots = 2 * di.sm_count;  // two CTAs fit an SM
   const int row_tiles = a.epi == kGemvNone ? (a.N + 15) / 16 : (a.N / 2 + 7) / 8;
@@ -510,7 +514,6 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream) {
   // against 30 with one; smaller products would leave SMs without rows).
   // Not with two tables: their shared memory and two row tiles' leave an SM one CTA
   // (8 x 4096 x 32768 NF4, blocks of 64, fp32 out 41.0 us against 45.9 with two row tiles).
-  const bool two = a.fmt == kGemvCodebook && a.out_f32 && a.quant != E4B_QUANT_FP4;
   const int rt = a.M <= 8 && !two && static_cast<int64_t>(row_tiles) * p.chunks >= 4ll * slots * kWarps ? 2 : 1;
   // The split of K over a CTA's warps that needs the fewest steps: chunks of a
   // warp's share, and about two for the sums that end a tile.

@@ -178,6 +178,26 @@ def test_a_bad_token_stays_in_its_row():
         assert torch.equal(out[keep], want[keep]) and not torch.isfinite(out[6].float()).any()
 
 
+@pytest.mark.parametrize("kind", ["nf4", "fp4", "int4"])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(1, 83, 384), (8, 100, 2048), (16, 83, 384), (8, 20021, 2048)])
+def test_an_infinity_keeps_its_sign(kind, out, M, N, K):
+    """One infinite x: the result is that infinity with the weight's sign, and NaN where the weight is zero."""
+    require_gpu()
+    handle, w = _weight(N, K, 32, kind, kind == "int4")
+    x = _x(M, K).clone()
+    x[M // 2, 70], x[M - 1, 300] = float("inf"), float("-inf")
+    y = torch.empty(M, N, dtype=out, device="cuda")
+    e4b.e4b_gemv_4bit(x, handle, y)
+    for row in {M // 2, M - 1}:
+        # 0 * inf is NaN, and so is a sum of two infinities of other signs
+        with np.errstate(invalid="ignore"):
+            terms = [float("inf") * w[:, 70]] * (row == M // 2) + [float("-inf") * w[:, 300]] * (row == M - 1)
+            want = sum(terms)
+        got = y[row].double().cpu().numpy()
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~np.isnan(want)], want[~np.isnan(want)])
+
+
 def test_no_tokens():
     require_gpu()
     handle, _ = _weight(96, 256, 32, "nf4")
