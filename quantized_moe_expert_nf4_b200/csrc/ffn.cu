@@ -125,7 +125,8 @@ __device__ __forceinline__ void act_both(int act, float g, float* a, float* da) 
     constexpr float k2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
     const float s = sigmoid_of(k2 * (g + 0.044715f * g * g * g));
     *a = g * s;
-    *da = s + g * s * (1.0f - s) * k2 * (1.0f + 0.134145f * g * g);
+    // far out s (1 - s) is 0, and g^2 may not become infinite before it is multiplied by that
+    *da = s + g * s * (1.0f - s) * k2 * (1.0f + 0.134145f * fminf(g * g, 1e30f));
   }
 }
 

@@ -173,6 +173,25 @@ def test_an_infinity_stays_in_its_row():
         assert torch.equal(out[keep], want[keep]) and not torch.isfinite(out[9].float()).any()
 
 
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [20, 700])
+def test_gradients_at_far_pre_activations(kind, M):
+    """Far out the activation is 0 or its argument, and its derivative 0 or 1, at any size of the pre-activation."""
+    require_gpu()
+    x, wgu, wd, dout = _inputs(M, 264, 136)
+    fn = e4b.GatedFFN(wgu, wd, ACT[kind])
+    pre = torch.randn(M, 272, device="cuda").to(BF)
+    for row, far in enumerate((30.0, 1e4, 1e10, 1e20, 1e25)):
+        pre[row, 7], pre[row, 99], pre[row + 6, 40] = far, -far, far
+    got = _backward(x, fn, pre, dout, ("dx", "dgate_up"))
+    want = ffn.backward(_np(x), _np(pre), _np(wgu), _np(wd), _np(dout), kind)
+    for k in ("dx", "dgate_up"):
+        g = _np(got[k])
+        assert np.all(np.isfinite(g))
+        # bf16 gradients of the pre-activations and of the result: 2^-8 / sqrt(3) each
+        assert np.linalg.norm(g - want[k]) <= 5e-3 * np.linalg.norm(want[k])
+
+
 def test_no_rows():
     require_gpu()
     x, wgu, wd, dout = _inputs(0, 64, 64)
