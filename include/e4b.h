@@ -513,7 +513,8 @@ typedef struct {
  * x [M, ldx] bf16 (ldx >= K, ldx % 8 == 0); out [M, ldo] of out_dtype.
  * Requires K a multiple of the group; any N >= 1, even with SwiGLU;
  * 0 <= M <= 16 (longer inputs: e4b_grouped_4bit_gemm() with one group).
- * fp32 accumulation; scales multiply group sums in fp32.  INT4 and FP4 values
+ * fp32 accumulation; scales multiply group sums in fp32, so |x| times a value
+ * (up to 15, 128 of them) has to stay in fp32's range: |x| < 2^116.  INT4 and FP4 values
  * are exact; NF4 entries are within 1.8e-3 with bf16 output and 2^-18 with
  * fp32 output.  Deterministic.  No workspace.  out may not overlap x.
  */
@@ -557,8 +558,9 @@ typedef struct {
  * (or NULL); n [M, H] of n_dtype; gate of gate_dtype in the shape of its kind.
  * r is written exactly when y is given, n exactly when w_next is; types and
  * leading dimensions of absent tensors are ignored.  Leading dimensions are in
- * elements, >= H.  Rows of any width and alignment are taken; H and leading
- * dimensions in multiples of 8 with 16-byte aligned bases are moved as vectors.
+ * elements, >= H.  Rows of any width and alignment to their elements are taken;
+ * fastest are H and leading dimensions in multiples of 8 with bases aligned to 8
+ * elements (16 bytes in bf16, 32 in fp32), then other rows in 16-byte aligned tensors.
  * r may be x and n may be y or x (same base, type and leading dimension).
  * Sums and both norms are taken in fp32, n from the unrounded r; each output
  * is rounded once.  M >= 0; no workspace; one launch.

@@ -9,11 +9,13 @@
 // Bound: HBM.  CTAs are persistent and take a row at a time; T threads share
 // it, each with VPT groups of 8 columns.  The rows ahead come through a ring of
 // cp.async stages in shared memory, so that loads stay in flight while a row's
-// sums meet (a warp shuffle and a block barrier per sum).  Where rows can be
-// moved as vectors, a thread copies and reads its own columns only; other rows
-// (odd widths, strides) are copied as the 16-byte units that they touch and
-// read by element.  Both norms are taken on 32-bit values in registers (n from the
-// unrounded r), and every output is rounded once.
+// sums meet (a warp shuffle and a block barrier per sum).  Where 8 columns of every row
+// are aligned vectors, a thread copies and reads its own columns only.  Rows that start
+// anywhere within 16 bytes (odd widths, odd strides) are copied as the 16-byte units
+// that they touch and read as shifted vectors.  Tensors that are not 16-byte aligned, and
+// rows too long for a ring of vectors (see plan()), are read by element.  Both norms
+// are taken on 32-bit values in registers (n from the unrounded r), and every output is
+// rounded once.
 //
 // Backward, with d = dr + (dn through the next norm):
 //   h = dn * (w_next + offset):  d += rstd_r * (h - rhat * mean(h * rhat))
@@ -27,13 +29,17 @@
 //
 // Measured (bandwidth of the bytes that a call cannot do without):
 //   forward, 8192 x 2880, bf16 y, fp32 stream, bf16 n   45-50 us, 5.7 TB/s
-//   forward, 8192 x 2880, all bf16                      36 us, 5.2 TB/s
-//   forward, 8192 x 2049, all bf16 (shifted)            70 us, 1.9 TB/s
-//   backward, 8192 x 2880, bf16, fp32 dgate and dw      61.4 us, 4.6 TB/s
-//   backward, 2048 x 2049 (shifted)                     45 us, 1.5 TB/s
+//   forward, 8192 x 2880, all bf16, channel gate        35 us, 5.3 TB/s
+//   forward, 8192 x 4096, all bf16, channel gate        64 us, 4.2 TB/s
+//   forward, 8192 x 2049, all bf16, no gate (shifted)   54 us, 2.5 TB/s
+//   backward, 8192 x 2880, bf16, fp32 dgate and dw      61.5 us, 4.6 TB/s
+//   backward, 8192 x 4096, the same                     144 us, 2.8 TB/s (see norm_shape())
+//   backward, 4096 x 8192, the same                     209 us, 1.9 TB/s
+//   backward, 2048 x 2049, full gate (shifted)          45 us, 1.5 TB/s
 //   forward of one row                                  2.6 us on the device, 9.5 with the call
-// The forward is bound by HBM.  The backward is bound by issue and by HBM about alike at 24
-// warps an SM (registers hold a thread's columns of the weights and their gradients).  What
+// The forward is bound by HBM.  The backward of one group of columns a thread is full
+// neither in issue (65%) nor in HBM (67%) at 24 warps an SM: registers (a thread's columns
+// of the weights and their gradients) allow no more, and shared memory is read twice a row.  What
 // carried it: rows ahead in a ring 265 -> 132 us, packed fp32 -> 104, kernels with the usual
 // inputs and outputs known at compile time -> 85, weights in registers and what is the same
 // in every row taken out of the sums over rows -> 61.  A row's sums meet once: the sum
@@ -320,9 +326,14 @@ __global__ void __launch_bounds__(kRedCols * kRedLanes) block_norm_reduce_kernel
   }
 }
 
+// A B200's SMs.  Not asked of the device: the workspace's size and the order of the sums over
+// rows follow from the arguments alone.
 constexpr int kSms = 148;
 
-// Threads of a row, their groups, and the persistent CTAs.
+// Threads of a row, their groups, and the CTAs: as many as threads_per_sm gives each SM, which
+// is what one group of columns a thread leaves room for.  With two and four groups the
+// backward's registers (136 and 128 a thread) let fewer of them run at a time (at 4096 columns one of
+// three, 144 us for 8192 rows in bf16), and the rest follow as these end.
 NormShape norm_shape(int64_t M, int H, int threads_per_sm, bool vec) {
   const int nvec = (H + 7) / 8;
   NormShape s{};
@@ -342,7 +353,9 @@ struct Moves {
 };
 
 // The shape, and the ring: as many stages (2 to 4) as leave room for the SM's other
-// CTAs, or, of rows too long for that, none.
+// CTAs, but two at least, even where an SM then holds fewer CTAs.  Where two stages do not fit
+// (the backward of 8192 columns with fp32 x and y) rows are read by element from memory,
+// without a ring: 4096 x 8192 1130 us, with bf16 y and a ring of vectors 284.
 Moved plan(NormArgs* a, NormShape* s, const Moves& moves, bool x_f32, bool y_f32, int threads_per_sm) {
   constexpr uint32_t kRoom = 216 * 1024;
   for (const Moved moved : {kVector, kShifted, kElements}) {

@@ -25,9 +25,11 @@
 // through the warp-MMA kernel of the 4-bit products instead.
 //
 // Measured, H = I = 2880, against cuBLAS's 1652 (burst) and 1388 (sustained) bf16 TFLOP/s
-// on the same GPUs: forward of 4096 tokens 169 us, 1.21 PFLOP/s; forward and backward of
-// 8192 tokens 1064 us in a loop of a second or more, 1.15 PFLOP/s (the power cap lowers the
-// clock), 925 us in a short one.  197 x 2048 x 776 takes 17 us (one tile and its epilogue
+// on the same GPUs: forward of 4096 tokens 175 us back to back, 1.17 PFLOP/s (149 us in a short
+// run); forward and backward of 8192 tokens 1105 us in a loop of a second or more, 1.11 PFLOP/s
+// (the power cap lowers the clock), 959 us in a short one.  256 tokens, forward and backward,
+// 129 us (floor 23: six launches of one tile a CTA).  One token at H = 4096, I = 11008 51 us,
+// 5.3 TB/s.  197 x 2048 x 776 takes 17 us (one tile and its epilogue
 // a kernel: latency), one token 8.7 us (two launches).  What the steps brought for
 // the long ones: loads and pieces as TMA 972 -> 944 us, tiles walked in groups of 8
 // rows 1140 -> 1085 sustained, overlapped launches 1.6%.

@@ -38,10 +38,14 @@
 //                                                      two or three chunks a warp
 //   13 x 2880 x 16411 FP4, blocks of 32               19.1 us (4.1)
 //   8 x 4096 x 32768 int4, blocks of 128, fp32 out    23.5 us (10.7): 3.0 TB/s
-// The large ones are bound by instruction issue with four warps a scheduler: the codes
-// alone take 32 (int4) to 59 (table) cycles for 16 rows x 32 k and scheduler, a half again for addresses,
-// scales and sums.  A copy of the kernel without 7 of 8 products took 15.5 us for the
-// last call, one without the copies 22.8.  Measured and not kept for it: x in shared
+//   1 x 4096 x 14336 int4, blocks of 128              13.2 us (4.6)
+//   8 x 4096 x 32768 NF4, blocks of 64, fp32 out      42 us (11.0): two tables
+// The large ones wait more than they issue, at four warps a scheduler: the last int4 call of 8
+// tokens has its issue slots 52% busy.  Codes and products take 32 (int4) to 59 (table)
+// cycles for 16 rows x 32 k and scheduler, 16 more for a second set of tokens: 6 of the FP4 call's 19 us.
+// A chunk's tokens (4 KB for 8, 8 KB for 16, beside 2 KB of codes a row tile) are loaded at its
+// head and used at once.  A copy of the kernel without 7 of 8 products took 15.5 us for the
+// int4 call, one without the copies 22.8.  Measured and not kept for it: x in shared
 // memory and 16 to 32 warps (26.6), a warp for the sums alone (39), all of K
 // by one warp (31.9: 128-byte pieces of 2 KB rows use DRAM pages badly), x read
 // again by every block (35), (chunk, row tile) items in equal runs with all sums
