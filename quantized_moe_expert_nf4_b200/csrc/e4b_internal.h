@@ -287,9 +287,11 @@ cudaError_t ensure_smem_limit(const void* func, size_t bytes);
 // Launches `kernel` so that it may start before the launch ahead of it in the stream has
 // ended (programmatic dependent launch): its CTAs take free SMs and set themselves up,
 // and it reads and writes nothing in memory before its own pdl_wait(), which returns when
-// all earlier work has ended and is visible.  Every kernel launched like this calls
+// all earlier work has ended and is visible.  A kernel launched like this calls
 // pdl_wait() and then pdl_launch_dependents(): the next may start once all CTAs
-// run and everything before this kernel has ended.  `cluster`: CTAs of a cluster.
+// run and everything before this kernel has ended.  Two kernels read earlier, within a call
+// whose first launch has waited: GemvArgs::after_input (weights), and the FFN's
+// kAfterNothing, which waits before it ends.  `cluster`: CTAs of a cluster.
 template <class... P, class... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), int grid, int block, size_t smem, int cluster, cudaStream_t stream,
                               const A&... args) {
