@@ -115,7 +115,8 @@ def _check_large(M, N, K, group, kind, zeros=False, scale_dtype=F32, out=BF, swi
     assert off.norm() <= (3e-3 if out == BF else 2e-5) * (2 if swiglu else 1) * want.norm()
 
 
-# A warp takes two row tiles from 32 * 296 (row tile, chunk of 256 codes) pairs on, at up to 8 tokens.  Row counts
+# A warp takes two row tiles from 32 * 296 (row tile, chunk of 256 codes) pairs on, at up to 8 tokens (one with NF4
+# and fp32 output).  Row counts
 # end inside a tile, and inside its second half; K ends inside a chunk, or not.
 @pytest.mark.parametrize("kind,group,zeros,scale_dtype", [
     ("nf4", 32, False, BF), ("nf4", 64, False, F32), ("nf4", 128, False, BF), ("fp4", 32, False, F32), ("fp4", 64, False, BF),
